@@ -417,6 +417,91 @@ KVATTN_API int kvattn_resident_update(const int32_t* sel_logical, const int32_t*
                                       const int32_t* extra_page, int32_t* page_list, int32_t* copy_host,
                                       int32_t* copy_dst, int32_t* n_copies, kvattn_stream_t stream);
 
+/* ---- ragged batches: several sequences over one cache ---------------------------------
+ * A serving step works on several sequences whose pages share the pools of one descriptor
+ * ([STREAM] method list: paged attention over single tokens and verify batches; [KVMEM] test
+ * command: 128-token blocks).  The three calls below take the same batch: kvattn_append_batch
+ * writes its tokens into their pages, kvattn_decode_batch attends from them, and
+ * kvattn_read_batch gives back the values that the cache holds for them.
+ *
+ * Element types of the token arrays. */
+enum kvattn_dtype { KVATTN_F32 = 0, KVATTN_F16 = 1, KVATTN_BF16 = 2 };
+
+/* A token array [n_rows][heads][256] in device memory: element (r, h, c) sits at
+ * data + r * row_stride + h * head_stride + c, strides in elements.  data is 16-byte aligned
+ * and strides are multiples of 16 bytes; a stride over a single row or head is not looked at.
+ * Inputs may overlap themselves (a stride of 0 repeats a row); the rows and heads of an output
+ * must not. */
+typedef struct kvattn_rows {
+  void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+  int32_t dtype;    /* enum kvattn_dtype */
+  int32_t reserved; /* must be 0         */
+} kvattn_rows;
+
+/* A ragged batch.  The tokens of sequence s are rows [row_start[s], row_start[s + 1]) of the
+ * token arrays; row r has position pos_start[s] + r - row_start[s].  The sequence holds the
+ * tokens at positions 0 .. pos_start[s] + rows - 1 once the call's own are appended.  A
+ * sequence may have no row; rows before row_start[0] and from row_start[n_seqs] on (a padded
+ * batch) are neither read nor written.
+ * Checked on the device, because the arrays live there: 0 <= row_start[s] <= row_start[s + 1]
+ * <= n_rows, at most max_rows rows, pos_start[s] >= 0 and the last position inside max_blocks
+ * blocks.  A sequence that breaks one of these is left out (none of its rows is written) and
+ * KVATTN_ERR_INVALID_ARG is recorded in the device error word. */
+typedef struct kvattn_batch {
+  const int32_t* row_start;  /* device int32 [n_seqs + 1], ascending                        */
+  const int32_t* pos_start;  /* device int32 [n_seqs]                                       */
+  const int32_t* page_table; /* device int32 [n_seqs][H_kv][max_blocks]: logical block ->   */
+                             /* physical page (entries no token needs are not read)         */
+  int64_t n_rows;            /* rows of the token arrays, < 2^31                            */
+  int32_t n_seqs;
+  int32_t max_rows;          /* the most rows of any sequence                               */
+  int32_t max_blocks;
+  int32_t reserved;          /* must be 0                                                   */
+} kvattn_batch;
+
+/* Quantizes every row of the batch and writes it into its page, by the rules of
+ * kvattn_quantize_append (16-bit inputs are widened to fp32 first, which is exact).  Other
+ * slots of the touched pages keep their bytes.  Every (page, slot) is written by at most one
+ * row of a call: two sequences may share pages only where neither writes.
+ *   k, v   [n_rows][H_kv][256], of one dtype */
+KVATTN_API int kvattn_append_batch(const kvattn_kv_desc* desc, const kvattn_batch* batch, const kvattn_rows* k,
+                                   const kvattn_rows* v, kvattn_stream_t stream);
+
+/* Writes the values that the cache holds for every row of the batch: code x scale (+ minimum),
+ * rounded to fp32 (exact without a minimum) and then to the output's type.  A row whose page
+ * id is out of range is written as zeros (and recorded).  k or v may be NULL: that side is
+ * then neither read nor written.
+ *   k, v   [n_rows][H_kv][256], of one dtype */
+KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch* batch, const kvattn_rows* k,
+                                 const kvattn_rows* v, kvattn_stream_t stream);
+
+/* Attention of every row of the batch, for every query head, over the pages of its sequence.
+ * A row at position P sees the keys at positions p <= P, and with window > 0 only those with
+ * p > P - window.  Slots past the sequence's last position, and blocks that no row's window
+ * reaches, are not used, whatever their bytes are.
+ *   q            [n_rows][H_q][256]
+ *   page_logical device int32 [n_seqs][H_kv][max_blocks]: the logical block of each entry of
+ *                page_table, which then is a list of pages in any order (a selection of
+ *                kvattn_select_blocks over n_seqs * H_kv units); NULL: entry i is block i
+ *   n_pages      device int32 [n_seqs][H_kv]: entries in use (clamped to [0, max_blocks]);
+ *                NULL without page_logical: as many as the sequence has blocks; NULL with it:
+ *                max_blocks
+ *   window       0: every key up to the row's own position
+ *   out          [n_rows][H_q][256] of q's dtype: softmax(q.k/16) v
+ *   lse          device fp32 [n_rows][H_q]: as for kvattn_decode (a row that sees no key: -inf,
+ *                out = 0)
+ *   ws           device workspace of kvattn_decode_batch_workspace_size() bytes, 256-byte
+ *                aligned; needs no initialisation.  Calls that share one must not overlap.
+ * Supports group * max_rows <= 24.  Results do not depend on the SM's timing: the split of
+ * the work depends on the lengths and the device alone. */
+KVATTN_API size_t kvattn_decode_batch_workspace_size(const kvattn_kv_desc* desc, const kvattn_batch* batch);
+KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batch* batch, const kvattn_rows* q,
+                                   const int32_t* page_logical, const int32_t* n_pages, int32_t window,
+                                   const kvattn_rows* out, float* lse, void* ws, size_t ws_bytes,
+                                   kvattn_stream_t stream);
+
 /* Polls `event` until it completes or timeout_ms elapses (KVATTN_ERR_TIMEOUT). */
 KVATTN_API int kvattn_stream_wait(kvattn_event_t event, int timeout_ms);
 

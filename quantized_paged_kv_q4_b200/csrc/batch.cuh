@@ -1,0 +1,115 @@
+// Ragged batches of sequences over one cache: the parameters that the append, read and decode
+// kernels share, and the device helpers that load, store and locate their rows.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace kvattn {
+
+// A token array [n_rows][heads][256], strides in elements.
+struct RowsView {
+  void* data;
+  long long row_stride, head_stride;
+};
+
+struct BatchParams {
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  int64_t k_stride, v_stride, n_pages;
+  const int32_t* row_start;
+  const int32_t* pos_start;
+  const int32_t* page_table;  // [n_seqs][n_kv][max_blocks]
+  long long n_rows;
+  int n_seqs, max_rows, max_blocks, n_kv;
+};
+
+// Eight consecutive elements of a row as fp32 (exact).
+template <typename T>
+__device__ __forceinline__ void load8(const void* data, long long at, float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(data) + at);
+    const float4 a = s[0], b = s[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const T*>(data) + at);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same_v<T, __half>) {
+        x[2 * i] = half_lo(w[i]);
+        x[2 * i + 1] = half_hi(w[i]);
+      } else {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+// Two fp32 -> two 16-bit elements in one word (lo in the low half), round to nearest.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (std::is_same_v<T, __half>) {
+    return pack_half2(lo, hi);
+  } else {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(void* data, long long at, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(data) + at);
+    d[0] = make_float4(x[0], x[1], x[2], x[3]);
+    d[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<T*>(data) + at) =
+        make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+  }
+}
+
+// One sequence of the batch, read and checked (kvattn_batch): rows [r0, r0 + rows) at
+// positions pos0 ...  A sequence that breaks a check has rows = 0 and is recorded.
+struct BatchSeq {
+  int r0, rows, pos0;
+};
+
+__device__ __forceinline__ BatchSeq load_seq(const BatchParams& p, int s, bool check_blocks) {
+  BatchSeq q;
+  const int r0 = p.row_start[s], r1 = p.row_start[s + 1], pos0 = p.pos_start[s];
+  const long long end = static_cast<long long>(pos0) + (static_cast<long long>(r1) - r0);
+  const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.n_rows && static_cast<long long>(r1) - r0 <= p.max_rows && pos0 >= 0 &&
+                  end <= INT32_MAX &&
+                  (!check_blocks || r1 == r0 || end <= static_cast<long long>(p.max_blocks) * kPageTokens);
+  q.r0 = r0;
+  q.rows = ok ? r1 - r0 : 0;
+  q.pos0 = pos0;
+  if (!ok) record_error(KVATTN_ERR_INVALID_ARG);
+  return q;
+}
+
+// The last sequence whose first row is <= row, by the whole warp (32 candidates a step): the
+// one that holds the row, unless the row lies in the padding (the caller checks).  -1: before
+// the first sequence.  Any contents of row_start keep the answer inside [-1, n_seqs).
+__device__ __forceinline__ int find_seq(const int32_t* row_start, int n_seqs, int row, int lane) {
+  int lo = 0, hi = n_seqs;
+  while (true) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool le = at < hi && row_start[at] <= row;
+    const int n = __popc(__ballot_sync(0xffffffffu, le));
+    if (n == 0) return lo == 0 ? -1 : lo;
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) return lo;
+  }
+}
+
+}  // namespace kvattn

@@ -8,3 +8,6 @@
 #include "stream.cu"
 #include "api.cu"
 #include "noalloc.cu"
+#include "batch_cache.cu"
+#include "batch_decode.cu"
+#include "batch_api.cu"

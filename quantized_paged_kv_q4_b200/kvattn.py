@@ -35,6 +35,7 @@ FMT_Q5_0 = 50
 FMT_Q4_1 = 41
 ROLE_K = 0
 ROLE_V = 1
+F32, F16, BF16 = 0, 1, 2
 FMT = {"q4_0": FMT_Q4_0, "q8_0": FMT_Q8_0, "q5_1": FMT_Q5_1, "q5_0": FMT_Q5_0, "q4_1": FMT_Q4_1}
 
 
@@ -51,6 +52,16 @@ class kvattn_kv_desc(ctypes.Structure):
         ("k_page_stride", c_int64), ("v_page_stride", c_int64), ("n_pages", c_int64),
         ("sm_budget", c_int32), ("reserved", c_int32),
     ]
+
+
+class kvattn_rows(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("row_stride", c_int64), ("head_stride", c_int64), ("dtype", c_int32),
+                ("reserved", c_int32)]
+
+
+class kvattn_batch(ctypes.Structure):
+    _fields_ = [("row_start", c_void_p), ("pos_start", c_void_p), ("page_table", c_void_p), ("n_rows", c_int64),
+                ("n_seqs", c_int32), ("max_rows", c_int32), ("max_blocks", c_int32), ("reserved", c_int32)]
 
 
 _SIGS = {
@@ -96,6 +107,14 @@ _SIGS = {
     "kvattn_resident_update": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int,
                                        c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                        c_void_p]),
+    "kvattn_append_batch": (c_int, [POINTER(kvattn_kv_desc), POINTER(kvattn_batch), POINTER(kvattn_rows),
+                                    POINTER(kvattn_rows), c_void_p]),
+    "kvattn_read_batch": (c_int, [POINTER(kvattn_kv_desc), POINTER(kvattn_batch), POINTER(kvattn_rows),
+                                  POINTER(kvattn_rows), c_void_p]),
+    "kvattn_decode_batch_workspace_size": (c_size_t, [POINTER(kvattn_kv_desc), POINTER(kvattn_batch)]),
+    "kvattn_decode_batch": (c_int, [POINTER(kvattn_kv_desc), POINTER(kvattn_batch), POINTER(kvattn_rows), c_void_p,
+                                    c_void_p, c_int32, POINTER(kvattn_rows), c_void_p, c_void_p, c_size_t,
+                                    c_void_p]),
 }
 
 _lib = None
@@ -165,6 +184,62 @@ def make_desc(n_kv_heads, n_q_heads, k_pool, v_pool, n_pages, v_fmt="q4_0", k_pa
     return kvattn_kv_desc(n_kv_heads, n_q_heads, head_dim, page_tokens, kf, vf, _d(k_pool), _d(v_pool),
                           k_page_stride or kvattn_page_bytes(ROLE_K, kf), v_page_stride or kvattn_page_bytes(ROLE_V, vf),
                           n_pages, sm_budget, 0)
+
+
+_DTYPES = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
+
+
+def _i32(x, what, shape=None):
+    """A device int32 array of the batch calls: a contiguous CUDA tensor (its shape checked where
+    one is given), a raw address or None."""
+    if x is None or isinstance(x, int):
+        return x
+    if str(x.dtype) != "torch.int32":
+        raise ValueError(f"{what}: expected int32, got {x.dtype}")
+    if shape is not None and tuple(x.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(x.shape)}")
+    return _d(x)
+
+
+def make_batch(row_start, pos_start, page_table, n_rows, max_rows) -> kvattn_batch:
+    """The batch whose sequence s owns rows [row_start[s], row_start[s + 1]) of token arrays of
+    n_rows rows, at positions pos_start[s] ..., with the pages page_table[s][h] (int32 CUDA tensors
+    [n_seqs + 1], [n_seqs] and [n_seqs][H_kv][max_blocks], which the caller keeps alive); no
+    sequence has more than max_rows rows."""
+    if page_table.dim() != 3:
+        raise ValueError(f"page_table: expected [n_seqs][H_kv][max_blocks], got {tuple(page_table.shape)}")
+    n_seqs, heads, max_blocks = page_table.shape
+    _one_device("make_batch", row_start, pos_start, page_table)
+    b = kvattn_batch(_i32(row_start, "row_start", (n_seqs + 1,)), _i32(pos_start, "pos_start", (n_seqs,)),
+                     _i32(page_table, "page_table"), n_rows, n_seqs, max_rows, max_blocks, 0)
+    b.heads, b.device = heads, page_table.device
+    return b
+
+
+def _one_device(what, *tensors):
+    """The batch calls launch on the current device: a tensor of another one is refused here."""
+    import torch
+
+    now = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.is_cuda and t.device.index != now:
+            raise ValueError(f"{what}: a tensor is on {t.device}, the current device is cuda:{now}")
+
+
+def make_rows(x, n_rows, heads) -> kvattn_rows:
+    """A token array [n_rows][heads][256] of fp32, fp16 or bf16 as the batch calls take it: any
+    strides over rows and heads (a slice of a fused projection, say), the channels contiguous."""
+    if not x.is_cuda:
+        raise ValueError(f"expected a CUDA tensor for a device-memory argument, got one on {x.device}")
+    if tuple(x.shape) != (n_rows, heads, 256):
+        raise ValueError(f"expected a token array of shape {(n_rows, heads, 256)}, got {tuple(x.shape)}")
+    dtype = _DTYPES.get(str(x.dtype))
+    if dtype is None:
+        raise ValueError(f"expected float32, float16 or bfloat16, got {x.dtype}")
+    rs, hs, cs = x.stride()
+    if cs != 1:
+        raise ValueError("expected contiguous channels (the last stride must be 1)")
+    return kvattn_rows(x.data_ptr(), rs, hs, dtype, 0)
 
 
 # ---------------------------------------------------------------- entry points
@@ -308,6 +383,48 @@ def kvattn_resident_update(sel_logical, n_sel, cap, n_units, n_blocks, n_full, s
                                         first_page, _d(extra_page), _d(page_list), _d(copy_host), _d(copy_dst),
                                         _d(n_copies), _s(stream)),
            "kvattn_resident_update")
+
+
+def _check_batch(what, desc, batch, *tensors):
+    if batch.heads != desc.n_kv_heads:
+        raise ValueError(f"{what}: page_table has {batch.heads} KV heads, the descriptor {desc.n_kv_heads}")
+    for t in tensors:
+        if t is not None and t.device != batch.device:
+            raise ValueError(f"{what}: a tensor is on {t.device}, the batch on {batch.device}")
+    _one_device(what, *tensors)
+
+
+def kvattn_append_batch(desc, batch, k, v, stream=None) -> None:
+    """Quantize-append every row of the batch into its page; k, v [n_rows][H_kv][256], of one of the
+    three types, with any strides over rows and heads."""
+    _check_batch("kvattn_append_batch", desc, batch, k, v)
+    kr, vr = (make_rows(x, batch.n_rows, desc.n_kv_heads) for x in (k, v))
+    _check(lib().kvattn_append_batch(desc, batch, kr, vr, _s(stream)), "kvattn_append_batch")
+
+
+def kvattn_read_batch(desc, batch, k=None, v=None, stream=None) -> None:
+    """The values that the cache holds for every row of the batch, into k and / or v
+    [n_rows][H_kv][256] (rows of no sequence are left as they were)."""
+    _check_batch("kvattn_read_batch", desc, batch, k, v)
+    kr, vr = (None if x is None else make_rows(x, batch.n_rows, desc.n_kv_heads) for x in (k, v))
+    _check(lib().kvattn_read_batch(desc, batch, kr, vr, _s(stream)), "kvattn_read_batch")
+
+
+def kvattn_decode_batch_workspace_size(desc, batch) -> int:
+    return lib().kvattn_decode_batch_workspace_size(desc, batch)
+
+
+def kvattn_decode_batch(desc, batch, q, out, lse, ws, page_logical=None, n_pages=None, window=0, stream=None) -> None:
+    """Attention of every row of the batch over its sequence's pages: q, out [n_rows][H_q][256] of one
+    type, lse fp32 [n_rows][H_q], ws a uint8 tensor of kvattn_decode_batch_workspace_size bytes."""
+    _check_batch("kvattn_decode_batch", desc, batch, q, out, lse, ws, page_logical, n_pages)
+    qr, outr = (make_rows(x, batch.n_rows, desc.n_q_heads) for x in (q, out))
+    if str(lse.dtype) != "torch.float32" or tuple(lse.shape) != (batch.n_rows, desc.n_q_heads):
+        raise ValueError(f"lse: expected float32 {(batch.n_rows, desc.n_q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
+    lists = (batch.n_seqs, batch.heads, batch.max_blocks)
+    _check(lib().kvattn_decode_batch(desc, batch, qr, _i32(page_logical, "page_logical", lists),
+                                     _i32(n_pages, "n_pages", lists[:2]), window, outr, _d(lse), _d(ws),
+                                     ws.numel() * ws.element_size(), _s(stream)), "kvattn_decode_batch")
 
 
 def _host_i32(a):
