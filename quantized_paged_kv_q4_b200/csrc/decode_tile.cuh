@@ -1,0 +1,361 @@
+// One 16-token tile of split-KV decode: the format traits of a (key, value) pair and the tile's
+// arithmetic, which the single-sequence and the ragged-batch decode share.
+#pragma once
+
+#include "common.cuh"
+
+namespace kvattn {
+
+constexpr int kTileBlocks = kBlocks;  // 32-channel blocks of a row
+
+// The regions of a K and a V page of a format pair.  Every region (codes, fifth bits, scales,
+// minima) is ordered by 16-token tile first, so tiles [g0, g1) of a page are one contiguous range
+// of each region: (offset of the region, bytes per tile).
+template <int KF, int VF>
+struct TileFormat {
+  static constexpr bool kK5 = KF == kKeyQ51 || KF == kKeyQ50;  // 5-bit key codes
+  static constexpr bool kKMin = KF == kKeyQ51;                 // keys with a zero point
+  static constexpr bool kVMin = VF == kValQ41;                 // values with a zero point
+  static constexpr int kKBytes =
+      KF == kKeyQ4 ? kK4PageBytes : KF == kKeyQ51 ? kK5PageBytes : KF == kKeyQ50 ? kK50PageBytes : kKPageBytes;
+  static constexpr int kKScaleOff = KF == kKeyQ4 ? kK4ScaleOffset : kK5 ? kK5ScaleOffset : kKScaleOffset;
+  static constexpr int kVBytes = VF == kValQ8 ? kV8PageBytes : VF == kValQ41 ? kV41PageBytes : kV4PageBytes;
+  static constexpr int kVScaleOff = VF == kValQ8 ? kV8ScaleOffset : kV4ScaleOffset;
+  static constexpr int kKRegions = KF == kKeyQ51 ? 4 : KF == kKeyQ50 ? 3 : 2;
+  static constexpr int kVRegions = VF == kValQ41 ? 3 : 2;
+  __host__ __device__ static constexpr int k_reg_off(int r) {
+    return r == 0 ? 0 : r == 1 ? (kK5 ? kK5HighOffset : kKScaleOff) : r == 2 ? kK5ScaleOffset : kK5MinOffset;
+  }
+  __host__ __device__ static constexpr int k_reg_tile(int r) {
+    return r == 0 ? (KF == kKeyQ8 ? 4096 : 2048) : r == 1 && kK5 ? 512 : 256;
+  }
+  __host__ __device__ static constexpr int v_reg_off(int r) { return r == 0 ? 0 : r == 1 ? kVScaleOff : kV41MinOffset; }
+  __host__ __device__ static constexpr int v_reg_tile(int r) { return r == 0 ? (VF == kValQ8 ? 4096 : 2048) : 256; }
+  static_assert(8 * (k_reg_tile(0) + k_reg_tile(1) + (kKRegions > 2 ? k_reg_tile(2) : 0) +
+                     (kKRegions > 3 ? k_reg_tile(3) : 0)) == kKBytes, "K regions");
+  static_assert(8 * (v_reg_tile(0) + v_reg_tile(1) + (kVRegions > 2 ? v_reg_tile(2) : 0)) == kVBytes, "V regions");
+  static_assert(k_reg_off(1) == 8 * k_reg_tile(0) && (kKRegions < 3 || k_reg_off(2) == k_reg_off(1) + 8 * k_reg_tile(1)) &&
+                (kKRegions < 4 || k_reg_off(3) == k_reg_off(2) + 8 * k_reg_tile(2)), "K region offsets");
+  static_assert(v_reg_off(1) == 8 * v_reg_tile(0) && (kVRegions < 3 || v_reg_off(2) == v_reg_off(1) + 8 * v_reg_tile(1)),
+                "V region offsets");
+};
+
+constexpr uint32_t kHalf2Magic = 0x64006400u;  // f16 1024.0 in both halves
+constexpr uint32_t kByte64x4 = 0x64646464u;    // high byte of f16 1024.0, for byte permutes
+constexpr uint32_t kHalf2_1032 = 0x64086408u;  // 1024 + 8
+constexpr uint32_t kHalf2_1040 = 0x64106410u;  // 1024 + 16
+constexpr uint32_t kHalf2_1152 = 0x64806480u;  // 1024 + 128
+constexpr uint32_t kHalf2_1_16 = 0x2C002C00u;  // 1/16
+constexpr uint32_t kHalf2_m72 = 0xD480D480u;   // -(64 + 8)
+constexpr uint32_t kHalf2_m64 = 0xD400D400u;   // -64
+constexpr uint32_t kHalf2_m80 = 0xD500D500u;   // -(64 + 16)
+constexpr uint32_t kHalf2_Sign = 0x80008000u;
+
+// B operand (probabilities times a per-token fp16 factor f) as an unevaluated f16 sum hi + lo:
+// hi = f16(ph * f); ph * f - hi is exact in f16 (an 11 x 11-bit product rounded to 11 bits
+// leaves at most 11 bits), and lo adds pl * f with one rounding.  hi + lo equals (ph + pl) * f
+// to about 2^-22 relative.
+__device__ __forceinline__ void split_scaled(uint32_t ph, uint32_t pl, uint32_t f, uint32_t& hi, uint32_t& lo) {
+  hi = hmul2(ph, f);
+  lo = hfma2(pl, f, hfma2(ph, f, hi ^ kHalf2_Sign));
+}
+
+// fp32 pair -> f16 hi part (round to nearest) and f16 lo part (the rounded remainder).
+__device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_half2(x0, x1);
+  lo = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
+}
+
+// P (its f16 parts) times the per-token scales f of a block: PP parts of the product.
+template <int PP>
+__device__ __forceinline__ void scale_p(uint32_t ph, uint32_t pl, uint32_t f, uint32_t& hi, uint32_t& lo) {
+  if constexpr (PP == 2) {
+    split_scaled(ph, pl, f, hi, lo);
+  } else {
+    hi = hmul2(ph, f);
+    lo = 0u;
+  }
+}
+
+// Where the parts of a page sit in a shared-memory copy: a whole page (tile G of it is read) ...
+template <int KF, int VF>
+struct PageLayout {
+  using F = TileFormat<KF, VF>;
+  static constexpr int kKScale = F::kKScaleOff, kKHigh = kK5HighOffset, kKMinimum = kK5MinOffset;
+  static constexpr int kVScale = F::kVScaleOff, kVMinimum = kV41MinOffset;
+};
+
+// ... or one tile by itself, its part of every region packed behind the one before (G = 0).
+template <int KF, int VF>
+struct SingleTileLayout {
+  using F = TileFormat<KF, VF>;
+  static constexpr int k_off(int r) { return r == 0 ? 0 : k_off(r - 1) + F::k_reg_tile(r - 1); }
+  static constexpr int v_off(int r) { return r == 0 ? 0 : v_off(r - 1) + F::v_reg_tile(r - 1); }
+  static constexpr int kKHigh = k_off(1), kKScale = F::kK5 ? k_off(2) : k_off(1), kKMinimum = k_off(3);
+  static constexpr int kVScale = v_off(1), kVMinimum = v_off(2);
+  static constexpr int kKBytes = k_off(F::kKRegions), kVBytes = v_off(F::kVRegions);
+};
+
+// Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
+// lane % 4; the thread's rows are 2t, 2t + 1).
+//   QP, PP       f16 parts of the query and of P: 2 keeps about 22 bits of each, 1 rounds once
+//   qfrag(b, ks) the query's B fragments of block b, k-step ks (hi0, hi1, lo0, lo1)
+//   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment
+//   crow         turns a dot product with the normalised row into a base-2 softmax score
+//   grow         how far, in powers of two, a score may pass the running maximum (p <= 2^grow)
+//   mask(e, x)   x, or -inf where the key is unseen: token g + 8 (e / 2), row 2t + e % 2
+// The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
+template <typename L, int KF, int VF, int QP, int PP, typename QFrag, typename Mask>
+__device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
+                                            uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], float grow,
+                                            Mask mask, float (&m_run)[2], float (&l_run)[2],
+                                            float (&oacc)[2 * kTileBlocks][4], float (&racc)[4]) {
+  using F = TileFormat<KF, VF>;
+  // ---------------- S = K Q^T over the 256 channels ----------------
+  // Key codes enter the MMA exactly (integers in f16).  Each 32-channel block is
+  // accumulated on its own (two k-steps, each with the query's parts) and then
+  // scaled by the block's fp32 scale into S; with a zero point, two more MMAs add the
+  // block minima times the query block sums.
+  float sacc[4] = {0.f, 0.f, 0.f, 0.f};
+  // key scales of rows g (H=0) and g+8 (H=1) for the 8 blocks, fp32; zero-point keys:
+  // the minima of blocks 2t, 2t + 1 of the same rows (the A fragment of the MMA that
+  // adds the minimum terms)
+  float dkf[2][kTileBlocks];
+  uint32_t mka[2] = {0u, 0u};
+#pragma unroll
+  for (int H = 0; H < 2; ++H) {
+    const uint32_t sa = kb + L::kKScale + (((G * 8 + g) * 2 + H) * 8) * 2;
+    uint32_t w[4];
+    const uint4 v = lds128(sa);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    if constexpr (F::kKMin) mka[H] = lds32(sa + (L::kKMinimum - L::kKScale) + 4 * t);
+#pragma unroll
+    for (int e = 0; e < kTileBlocks / 2; ++e) {
+      dkf[H][2 * e] = half_lo(w[e]);
+      dkf[H][2 * e + 1] = half_hi(w[e]);
+    }
+  }
+  // one block: an MMA per k-step and query part into xb, then S += d * xb
+  auto block_qk = [&](int bl, const uint32_t (&A)[2][4]) {
+    float xb[4];
+    const uint4 f0 = qfrag(bl, 0), f1 = qfrag(bl, 1);
+    mma_f16_z(xb, A[0][0], A[0][1], A[0][2], A[0][3], f0.x, f0.y);
+    if constexpr (QP == 2) mma_f16(xb, A[0][0], A[0][1], A[0][2], A[0][3], f0.z, f0.w);
+    mma_f16(xb, A[1][0], A[1][1], A[1][2], A[1][3], f1.x, f1.y);
+    if constexpr (QP == 2) mma_f16(xb, A[1][0], A[1][1], A[1][2], A[1][3], f1.z, f1.w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sacc[e] = fmaf(dkf[e >> 1][bl], xb[e], sacc[e]);
+  };
+  if constexpr (KF == kKeyQ8) {
+#pragma unroll
+    for (int P = 0; P < kTileBlocks / 2; ++P) {
+      const uint4 ka = lds128(kb + ((((G * 4 + P) * 2 + 0) * 8 + g) * 4 + t) * 16);
+      const uint4 kc = lds128(kb + ((((G * 4 + P) * 2 + 1) * 8 + g) * 4 + t) * 16);
+      // code bytes are offset-binary (q + 128)
+      const uint32_t wg[4] = {ka.x, ka.y, ka.z, ka.w};
+      const uint32_t w8[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t A[2][4];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          // exact code -> f16: 1024 + (q + 128) - 1152
+          A[ks][0] = hsub2(prmt(wg[2 * e + ks], kByte64x4, 0x4140u), kHalf2_1152);
+          A[ks][2] = hsub2(prmt(wg[2 * e + ks], kByte64x4, 0x4342u), kHalf2_1152);
+          A[ks][1] = hsub2(prmt(w8[2 * e + ks], kByte64x4, 0x4140u), kHalf2_1152);
+          A[ks][3] = hsub2(prmt(w8[2 * e + ks], kByte64x4, 0x4342u), kHalf2_1152);
+        }
+        block_qk(2 * P + e, A);
+      }
+    }
+  } else {
+    // 4- and 5-bit keys: one 32-bit word per (token, block) and lane holds channels 8t + i,
+    // channel i at bit 4 * (i / 2) + 16 * (i % 2); a shift by 8 * ks and two masks give
+    // the f16 pairs (4ks, 4ks + 1) and (4ks + 2, 4ks + 3) of k-step ks (1024 + q and
+    // 1024 + 16q).  5-bit keys: the fifth bits of the lane's four blocks of one token
+    // sit in one word, channel (c, i) at bit 16(i%2) + 4c + i/2, and are shifted to bit 4
+    // or bit 8 of each half.  The code (minus 8 for Q4_0, 16 for Q5_0) is exact in f16.
+#pragma unroll
+    for (int Q = 0; Q < 2; ++Q) {
+      const int row0 = (((G * 2 + Q) * 2 + 0) * 8 + g) * 4 + t;
+      const int row1 = (((G * 2 + Q) * 2 + 1) * 8 + g) * 4 + t;
+      const uint4 ka = lds128(kb + row0 * 16);
+      const uint4 kc = lds128(kb + row1 * 16);
+      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w};
+      const uint32_t wc[4] = {kc.x, kc.y, kc.z, kc.w};
+      uint32_t xa5 = 0, xc5 = 0;
+      if constexpr (F::kK5) {
+        xa5 = lds32(kb + L::kKHigh + row0 * 4);
+        xc5 = lds32(kb + L::kKHigh + row1 * 4);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t A[2][4];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const uint32_t xa = wa[c] >> (8 * ks), xc = wc[c] >> (8 * ks);
+          if constexpr (KF == kKeyQ4) {
+            A[ks][0] = hsub2(and_or(xa, 0x000F000Fu, kHalf2Magic), kHalf2_1032);
+            A[ks][2] = hfma2(and_or(xa, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kHalf2_m72);
+            A[ks][1] = hsub2(and_or(xc, 0x000F000Fu, kHalf2Magic), kHalf2_1032);
+            A[ks][3] = hfma2(and_or(xc, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kHalf2_m72);
+          } else {
+            const int slo = 4 - (4 * c + 2 * ks), shi = 7 - (4 * c + 2 * ks);
+            const uint32_t ha_lo = slo >= 0 ? xa5 << slo : xa5 >> -slo;
+            const uint32_t ha_hi = shi >= 0 ? xa5 << shi : xa5 >> -shi;
+            const uint32_t hc_lo = slo >= 0 ? xc5 << slo : xc5 >> -slo;
+            const uint32_t hc_hi = shi >= 0 ? xc5 << shi : xc5 >> -shi;
+            constexpr uint32_t kSubLo = KF == kKeyQ50 ? kHalf2_1040 : kHalf2Magic;
+            constexpr uint32_t kAddHi = KF == kKeyQ50 ? kHalf2_m80 : kHalf2_m64;
+            A[ks][0] = hsub2(or_and(and_or(xa, 0x000F000Fu, kHalf2Magic), ha_lo, 0x00100010u), kSubLo);
+            A[ks][2] = hfma2(or_and(and_or(xa, 0x00F000F0u, kHalf2Magic), ha_hi, 0x01000100u), kHalf2_1_16,
+                             kAddHi);
+            A[ks][1] = hsub2(or_and(and_or(xc, 0x000F000Fu, kHalf2Magic), hc_lo, 0x00100010u), kSubLo);
+            A[ks][3] = hfma2(or_and(and_or(xc, 0x00F000F0u, kHalf2Magic), hc_hi, 0x01000100u), kHalf2_1_16,
+                             kAddHi);
+          }
+        }
+        block_qk(4 * Q + c, A);
+      }
+    }
+  }
+  if constexpr (F::kKMin) {
+    // S += sum_b m[token][b] qsum[b][row] as one MMA per part of the block sums: A =
+    // the minima (tokens g, g + 8 x blocks 2t, 2t + 1; k = 8..15 is zero, exact in f16),
+    // B = the block sums of the query rows; the products accumulate in fp32
+    mma_f16(sacc, mka[0], mka[1], 0u, 0u, qsb_hi, 0u);
+    mma_f16(sacc, mka[0], mka[1], 0u, 0u, qsb_lo, 0u);
+  }
+  // ---------------- online softmax (base 2) ----------------
+  // The running maximum m_run of a row is shared by the 8 lanes that hold the row.
+  // It only has to bound the scores to within 2^grow (p <= 2^grow in f16), so the exact
+  // cross-lane maximum is computed only when some lane sees a score above
+  // m_run + grow: one warp vote per tile instead of three shuffles per row.
+  float sv[4], lm[2];
+  bool need = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    sv[e] = mask(e, sacc[e] * crow[e & 1]);
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    lm[c] = fmaxf(sv[c], sv[c + 2]);
+    need |= lm[c] > m_run[c] + grow;
+  }
+  if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float mx = lm[c];
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      if (mx > m_run[c] + grow) {
+        const float alpha = fast_exp2(m_run[c] - mx);  // 0 when m_run = -inf
+        l_run[c] *= alpha;
+#pragma unroll
+        for (int mt = 0; mt < 2 * kTileBlocks; ++mt) {
+          oacc[mt][c] *= alpha;
+          oacc[mt][c + 2] *= alpha;
+        }
+        if constexpr (F::kVMin) racc[c] *= alpha;
+        m_run[c] = mx;
+      }
+    }
+  }
+  // P as f16 parts, transposed in registers into B fragments
+  uint32_t pbh[2], pbl[2] = {0u, 0u};
+  {
+    float pr[4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float mu = m_run[c] == -INFINITY ? 0.f : m_run[c];
+      pr[c] = fast_exp2(sv[c] - mu);
+      pr[c + 2] = fast_exp2(sv[c + 2] - mu);
+      l_run[c] += pr[c] + pr[c + 2];
+    }
+    if constexpr (PP == 2) {
+      uint32_t h01, l01, h23, l23;
+      split_pair(pr[0], pr[1], h01, l01);
+      split_pair(pr[2], pr[3], h23, l23);
+      pbh[0] = movmatrix_t(h01);
+      pbh[1] = movmatrix_t(h23);
+      pbl[0] = movmatrix_t(l01);
+      pbl[1] = movmatrix_t(l23);
+    } else {
+      pbh[0] = movmatrix_t(pack_half2(pr[0], pr[1]));
+      pbh[1] = movmatrix_t(pack_half2(pr[2], pr[3]));
+    }
+  }
+  // ---------------- O^T += V^T P^T ----------------
+  // V codes enter the MMA exactly; the per-token block scale multiplies P (in PP f16
+  // parts), PP MMAs per 16-dimension half.
+  if constexpr (VF != kValQ8) {
+#pragma unroll
+    for (int Cc = 0; Cc < kTileBlocks / 2; ++Cc) {
+      const uint4 vw = lds128(vb + ((((G * 4 + Cc) * 8 + g) * 4 + t) * 16));
+      const uint32_t sidx = vb + L::kVScale + (((G * 4 + t) * 8 + 2 * Cc) * 4) * 2;
+      const uint4 dv = lds128(sidx);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int bl = 2 * Cc + e;
+        const uint32_t W0 = e ? vw.z : vw.x, W1 = e ? vw.w : vw.y;
+        const uint32_t d0 = e ? dv.z : dv.x, d1 = e ? dv.w : dv.y;
+        const uint32_t W0s = W0 >> 8, W1s = W1 >> 8;
+        // Q4_0: q - 8 (1024 + q - 1032, or (1024 + 16q) / 16 - 72); Q4_1: q
+        constexpr uint32_t kSubLo = F::kVMin ? kHalf2Magic : kHalf2_1032;
+        constexpr uint32_t kAddHi = F::kVMin ? kHalf2_m64 : kHalf2_m72;
+        const uint32_t a00 = hsub2(and_or(W0, 0x000F000Fu, kHalf2Magic), kSubLo);
+        const uint32_t a01 = hfma2(and_or(W0, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi);
+        const uint32_t a02 = hsub2(and_or(W1, 0x000F000Fu, kHalf2Magic), kSubLo);
+        const uint32_t a03 = hfma2(and_or(W1, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi);
+        const uint32_t a10 = hsub2(and_or(W0s, 0x000F000Fu, kHalf2Magic), kSubLo);
+        const uint32_t a11 = hfma2(and_or(W0s, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi);
+        const uint32_t a12 = hsub2(and_or(W1s, 0x000F000Fu, kHalf2Magic), kSubLo);
+        const uint32_t a13 = hfma2(and_or(W1s, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi);
+        uint32_t bh0, bl0, bh1, bl1;
+        scale_p<PP>(pbh[0], pbl[0], d0, bh0, bl0);
+        scale_p<PP>(pbh[1], pbl[1], d1, bh1, bl1);
+        mma_f16(oacc[2 * bl], a00, a01, a02, a03, bh0, bh1);
+        if constexpr (PP == 2) mma_f16(oacc[2 * bl], a00, a01, a02, a03, bl0, bl1);
+        mma_f16(oacc[2 * bl + 1], a10, a11, a12, a13, bh0, bh1);
+        if constexpr (PP == 2) mma_f16(oacc[2 * bl + 1], a10, a11, a12, a13, bl0, bl1);
+      }
+    }
+    if constexpr (F::kVMin) {
+      // sum over the tile's tokens of p * m for all 8 blocks at once: A = the minima
+      // (block g x tokens 2t, 2t + 1 | 2t + 8, 2t + 9, exact in f16; blocks 8..15 zero),
+      // B = P^T as its high and low parts
+      uint32_t m01, m89;
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                   : "=r"(m01), "=r"(m89)
+                   : "r"(vb + L::kVMinimum + (((G * 4 + t) * 8 + g) * 4) * 2));
+      mma_f16(racc, m01, 0u, m89, 0u, pbh[0], pbh[1]);
+      if constexpr (PP == 2) mma_f16(racc, m01, 0u, m89, 0u, pbl[0], pbl[1]);
+    }
+  } else {
+#pragma unroll
+    for (int b = 0; b < kTileBlocks; ++b) {
+      const uint4 vw = lds128(vb + ((((G * 8 + b) * 8 + g) * 4 + t) * 16));
+      uint32_t d0, d1;
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                   : "=r"(d0), "=r"(d1)
+                   : "r"(vb + L::kVScale + (((G * 4 + t) * 8 + b) * 4) * 2));
+      const uint32_t w[4] = {vw.x, vw.y, vw.z, vw.w};  // offset-binary code bytes (q + 128)
+      uint32_t a[4][2];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        a[q][0] = hsub2(prmt(w[q], kByte64x4, 0x4140u), kHalf2_1152);
+        a[q][1] = hsub2(prmt(w[q], kByte64x4, 0x4342u), kHalf2_1152);
+      }
+      uint32_t bh0, bl0, bh1, bl1;
+      scale_p<PP>(pbh[0], pbl[0], d0, bh0, bl0);
+      scale_p<PP>(pbh[1], pbl[1], d1, bh1, bl1);
+      mma_f16(oacc[2 * b], a[0][0], a[0][1], a[1][0], a[1][1], bh0, bh1);
+      if constexpr (PP == 2) mma_f16(oacc[2 * b], a[0][0], a[0][1], a[1][0], a[1][1], bl0, bl1);
+      mma_f16(oacc[2 * b + 1], a[2][0], a[2][1], a[3][0], a[3][1], bh0, bh1);
+      if constexpr (PP == 2) mma_f16(oacc[2 * b + 1], a[2][0], a[2][1], a[3][0], a[3][1], bl0, bl1);
+    }
+  }
+}
+
+}  // namespace kvattn
