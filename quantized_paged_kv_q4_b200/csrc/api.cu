@@ -19,6 +19,7 @@ cudaError_t launch_resident_update(const int32_t*, const int32_t*, int, int, int
                                    const int32_t*, int64_t, const int32_t*, int32_t*, int32_t*, int32_t*, int32_t*,
                                    cudaStream_t);
 cudaError_t prepare_prefill_kernels();
+cudaError_t prepare_batch_kernels();
 bool prefill_pair_supported(int key_fmt, int val_fmt);
 struct PrefillParams;
 cudaError_t launch_merge_lse(const float*, const float*, int, int, int, float*, float*, int, cudaStream_t);
@@ -160,6 +161,7 @@ KVATTN_API int kvattn_init(int device) {
   if (device < 0 || device >= kMaxDevices) return KVATTN_ERR_INVALID_ARG;
   cudaError_t e = cudaSetDevice(device);
   if (e != cudaSuccess) return cuda_fail(e);
+  if (g_inited[device]) return KVATTN_OK;  // the device's attributes and the kernels' are set once
   cudaDeviceProp prop;
   e = cudaGetDeviceProperties(&prop, device);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -168,6 +170,7 @@ KVATTN_API int kvattn_init(int device) {
   if ((e = prepare_select_kernels()) != cudaSuccess) return cuda_fail(e);
   if ((e = prepare_prefill_kernels()) != cudaSuccess) return cuda_fail(e);
   if ((e = prepare_resident_kernels()) != cudaSuccess) return cuda_fail(e);
+  if ((e = prepare_batch_kernels()) != cudaSuccess) return cuda_fail(e);
   g_sm_count[device] = prop.multiProcessorCount;
   g_inited[device] = true;
   return KVATTN_OK;

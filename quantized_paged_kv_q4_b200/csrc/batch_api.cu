@@ -1,4 +1,6 @@
 // C ABI of the ragged-batch calls: argument validation and launches.
+#include <algorithm>
+
 #include "batch.cuh"
 #include "decode.cuh"
 
@@ -61,6 +63,27 @@ BatchParams params_of(const kvattn_kv_desc* d, const kvattn_batch* b) {
   return p;
 }
 
+// The workspace of a decode: the plan's header, the first tile of every unit, two partials per CTA.
+struct BatchPlan {
+  int sms;
+  long long most_tiles;  // of all units together
+  size_t start_off, lse_off, o_off, bytes;
+};
+
+BatchPlan plan_batch(const kvattn_kv_desc* d, const kvattn_batch* b) {
+  BatchPlan p{};
+  p.sms = sm_budget_of(d);
+  const long long units = static_cast<long long>(b->n_seqs) * d->n_kv_heads;
+  p.most_tiles = units * 8 * std::max(b->max_blocks, 1);
+  const int row_tiles = batch_row_tiles(d->n_q_heads / d->n_kv_heads * std::max(b->max_rows, 1));
+  const size_t slots = static_cast<size_t>(batch_grid_bound(p.sms, row_tiles)) * 2 * row_tiles * 8;
+  p.start_off = 256;
+  p.lse_off = round_up(p.start_off + sizeof(long long) * units, 256);
+  p.o_off = round_up(p.lse_off + sizeof(float) * slots, 256);
+  p.bytes = p.o_off + sizeof(float) * slots * kHeadDim;
+  return p;
+}
+
 bool nothing_to_do(const kvattn_batch* b) { return b->n_seqs == 0 || b->n_rows == 0 || b->max_rows == 0; }
 
 }  // namespace
@@ -108,7 +131,7 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
 
 KVATTN_API size_t kvattn_decode_batch_workspace_size(const kvattn_kv_desc* desc, const kvattn_batch* batch) {
   if (validate_batch(desc, batch)) return 0;
-  return 256;
+  return plan_batch(desc, batch).bytes;
 }
 
 KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batch* batch, const kvattn_rows* q,
@@ -126,9 +149,10 @@ KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batc
   if ((st = validate_rows(out, batch->n_rows, desc->n_q_heads, true))) return st;
   if (q->dtype != out->dtype) return KVATTN_ERR_UNSUPPORTED_FORMAT;
   if (!lse) return KVATTN_ERR_INVALID_ARG;
-  const size_t need = kvattn_decode_batch_workspace_size(desc, batch);
+  const BatchPlan plan = plan_batch(desc, batch);
+  if (plan.most_tiles > (1ll << 38)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return KVATTN_ERR_INVALID_ARG;
-  if (ws_bytes < need) return KVATTN_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < plan.bytes) return KVATTN_ERR_WORKSPACE_TOO_SMALL;
   int dev;
   if ((st = current_device_checked(&dev))) return st;
   BatchDecodeParams p{};
@@ -140,9 +164,13 @@ KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batc
   p.n_list = n_pages;
   p.group = group;
   p.window = window;
-  p.ws = static_cast<uint8_t*>(ws);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.share = reinterpret_cast<long long*>(w);
+  p.unit_start = reinterpret_cast<long long*>(w + plan.start_off);
+  p.part_lse = reinterpret_cast<float*>(w + plan.lse_off);
+  p.part_o = reinterpret_cast<float*>(w + plan.o_off);
   const cudaError_t e = launch_decode_batch(p, q->dtype, key_format_id(desc->k_fmt), value_format_id(desc->v_fmt),
-                                            static_cast<cudaStream_t>(stream));
+                                            plan.sms, plan.most_tiles, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVATTN_OK : cuda_fail(e);
 }
 

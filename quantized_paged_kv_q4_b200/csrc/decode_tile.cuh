@@ -89,8 +89,8 @@ struct PageLayout {
 template <int KF, int VF>
 struct SingleTileLayout {
   using F = TileFormat<KF, VF>;
-  static constexpr int k_off(int r) { return r == 0 ? 0 : k_off(r - 1) + F::k_reg_tile(r - 1); }
-  static constexpr int v_off(int r) { return r == 0 ? 0 : v_off(r - 1) + F::v_reg_tile(r - 1); }
+  __host__ __device__ static constexpr int k_off(int r) { return r == 0 ? 0 : k_off(r - 1) + F::k_reg_tile(r - 1); }
+  __host__ __device__ static constexpr int v_off(int r) { return r == 0 ? 0 : v_off(r - 1) + F::v_reg_tile(r - 1); }
   static constexpr int kKHigh = k_off(1), kKScale = F::kK5 ? k_off(2) : k_off(1), kKMinimum = k_off(3);
   static constexpr int kVScale = v_off(1), kVMinimum = v_off(2);
   static constexpr int kKBytes = k_off(F::kKRegions), kVBytes = v_off(F::kVRegions);

@@ -81,6 +81,13 @@ class BatchCache:
         fmt, x = (self.k_fmt, self.k) if which == "k" else (self.v_fmt, self.v)
         return oq.dequantize(*oq.quantize(x[s][:, h], fmt), fmt)
 
+    def codes(self, s, h):
+        """|code| (the whole number that multiplies the block's scale) and |scale| of the sequence's values."""
+        q, d = oq.quantize(self.v[s][:, h], self.v_fmt)
+        d = np.abs((d if d.ndim == 2 else d[..., 0]).astype(np.float64))
+        return (np.abs(q.astype(np.int64) - (8 if self.v_fmt == "q4_0" else 0)).reshape(-1, 256),
+                np.repeat(d, 32, axis=-1))
+
 
 def put_tokens(page, role, fmt, x, slot):
     """The page bytes after tokens x [n][256] were encoded into slots slot, slot + 1, ..."""
@@ -103,9 +110,15 @@ def put_tokens(page, role, fmt, x, slot):
     return (page & ~mask) | (new & mask)
 
 
-def attend_rows(q, k, v, seen):
-    """Exact attention of rows q [n][256] over keys k, v [T][256] where seen [n][T]: (o, lse, sum p |v|,
-    max_t sum_c |q k| / 16), float64."""
+def attend_rows(q, k, v, seen, codes, scales):
+    """Exact attention of rows q [n][256] over keys k, v [T][256] where seen [n][T], float64: (o, lse,
+    sum p max(|v|, |code x scale|), max_t sum_c |q k| / 16, the sum that f16's smallest step can add,
+    below).  codes, scales [T][256]: |code| and |scale| of every value.
+
+    P enters the MMAs relative to the running maximum, which is within 2^2 of the row's own, so the
+    largest P is >= 1 and the sum of P is >= 1 / max p with p normalised.  Its f16 parts, and those of
+    P x scale, end at f16's subnormal step 2^-24: a key's P is off by up to 2^-25 and its product by up to
+    2 x 2^-25 (a high and a low part), whatever their size, times |v| and |code|."""
     q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
     s = np.where(seen, q @ k.T / 16.0, -np.inf)
     big = np.abs(q) @ np.abs(k).T / 16.0
@@ -117,20 +130,24 @@ def attend_rows(q, k, v, seen):
     p = p / safe[:, None]
     with np.errstate(divide="ignore"):
         lse = np.where(live, m + np.log(safe), -np.inf)
-    return p @ np.where(seen.any(0)[:, None], v, 0), lse, p @ np.abs(np.where(seen.any(0)[:, None], v, 0)), np.max(np.where(seen, big, 0), axis=1, initial=0)
+    v = np.where(seen.any(0)[:, None], v, 0)
+    floor = (seen @ np.abs(codes) * 2.0 ** -24 + seen @ np.abs(v) * 2.0 ** -25) * p.max(1, initial=0)[:, None]
+    return p @ v, lse, p @ np.maximum(np.abs(v), codes * scales), np.max(np.where(seen, big, 0), axis=1, initial=0), floor
 
 
-def check_attention(o, lse, o_ref, lse_ref, pv, big, n_keys, dtype):
+def check_attention(o, lse, o_ref, lse_ref, pv, big, floor, n_keys, dtype):
     """Bounds by arithmetic.  A score is a sum of 256 products of a query held to 22 bits (error <=
     2^-22 of sum |q k| / 16 = big) accumulated in fp32 over 8 blocks of 4 MMAs, each step within
     2^-24 of the running sum (< 2^-19 big with the scaling); the exponential adds 2^-21 relative,
     so a weight is off by ew = 2^-18 big + 2^-21 relative, in the numerator and in the sum.  The
-    output accumulates one MMA step per 16 keys and a merge, each 2^-24 of pv = sum p |v|.
-    bf16 outputs take P, and P times the value's scale, rounded to f16: 2 x 2^-12 pv.  The store
-    rounds once."""
+    output accumulates one MMA step per 16 keys and a merge, each 2^-24 of the sum of p times what is
+    added: code x scale, and a minimum where the format has one, each at most 2 pv, with pv = sum p
+    max(|v|, |code x scale|).  bf16 outputs take P (2^-12 of p |v|), and P times the value's scale (2^-12
+    of p |code x scale|), rounded to f16: 2^-11 pv.  f16's smallest step adds `floor` (attend_rows).  The
+    store rounds once."""
     ew = 2.0 ** -18 * big + 2.0 ** -21
-    acc = (n_keys / 16 + 64) * 2.0 ** -24
-    tol = (2 * ew + acc + (2.0 ** -11 if dtype == "bfloat16" else 2.0 ** -20))[:, None] * pv
+    acc = 4 * (n_keys / 16 + 64) * 2.0 ** -24
+    tol = (2 * ew + acc + (2.0 ** -11 if dtype == "bfloat16" else 2.0 ** -20))[:, None] * pv + floor
     tol = tol + EPS[dtype] * (np.abs(o_ref) + tol) + 1e-30
     # f16 has no more than its smallest subnormal step below 2^-14
     tol = tol + (2.0 ** -25 if dtype == "float16" else 0)

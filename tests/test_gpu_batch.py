@@ -159,10 +159,10 @@ def check_decode(c, name, qx, out, lse, window=0, listed=None):
             for h in range(c.H):
                 ok = seen if listed is None else seen & np.isin(pos // 128, listed(s, h))
                 rows_q = qx[r, h * c.group:(h + 1) * c.group]
-                o, l, pv, big = attend_rows(rows_q, c.held(s, h, "k"), c.held(s, h, "v"),
-                                            np.broadcast_to(ok, (c.group, ok.size)))
-                check_attention(out[r, h * c.group:(h + 1) * c.group], lse[r, h * c.group:(h + 1) * c.group], o, l, pv,
-                                big, int(ok.sum()), name)
+                ref = attend_rows(rows_q, c.held(s, h, "k"), c.held(s, h, "v"),
+                                  np.broadcast_to(ok, (c.group, ok.size)), *c.codes(s, h))
+                check_attention(out[r, h * c.group:(h + 1) * c.group], lse[r, h * c.group:(h + 1) * c.group], *ref,
+                                int(ok.sum()), name)
 
 
 @pytest.mark.parametrize("k_fmt,v_fmt", PAIRS)
@@ -253,7 +253,7 @@ def test_decode_same_result_every_time_and_in_any_place(kv_gpu):
 
 @pytest.mark.parametrize("k_fmt,v_fmt", PAIRS)
 def test_decode_large_and_small_values(kv_gpu, k_fmt, v_fmt):
-    """Values up to the top of fp16's range, and a thousandth: P times the scale stays in f16."""
+    """Values up to the top of fp16's range, and a thousandth: P times the scale stays finite in f16."""
     for scale in (6e4, 1e-3):
         c = BatchCache([(200, 2), (0, 1)], 1, 4, k_fmt, v_fmt, 28)
         for s in range(2):
@@ -261,20 +261,10 @@ def test_decode_large_and_small_values(kv_gpu, k_fmt, v_fmt):
             for b in range((len(c.v[s]) + 127) // 128):
                 page = c.table[s, 0, b]
                 c.v_bytes[page] = put_tokens(c.v_bytes[page], "v", v_fmt, c.v[s][128 * b:128 * b + 128, 0], 0)
-        qx, out, lse = run_decode(kv_gpu, c, "float32")
-        assert np.isfinite(out).all()
-        check = scale > 1
-        for s, (ctx, rows) in enumerate(c.lens):
-            for i in range(rows):
-                r = c.row_start[s] + i
-                ok = np.broadcast_to(np.arange(ctx + rows) <= ctx + i, (4, ctx + rows))
-                o, l, pv, big = attend_rows(qx[r], c.held(s, 0, "k"), c.held(s, 0, "v"), ok)
-                if check:
-                    check_attention(out[r], lse[r], o, l, pv, big, int(ok[0].sum()), "float32")
-                else:
-                    # the f16 parts of P x scale end at 2^-25 absolute per key and code (|code| <= 127)
-                    tol = (2.0 ** -17 * (big.max() + 1)) * pv + ok[0].sum() * 127 * 2.0 ** -25 / 1.0
-                    assert (np.abs(out[r] - o) <= tol).all()
+        for name in ("float32", "bfloat16"):
+            qx, out, lse = run_decode(kv_gpu, c, name)
+            assert np.isfinite(out).all()
+            check_decode(c, name, qx, out, lse)
 
 
 def test_decode_peaked_scores(kv_gpu):
@@ -368,7 +358,7 @@ class BatchCacheView:
     def __init__(self, c, n):
         self.__dict__.update(c.__dict__)
         self.lens = c.lens[:n]
-        self.held = c.held
+        self.held, self.codes = c.held, c.codes
 
 
 def test_empty_calls(kv_gpu):
@@ -455,7 +445,8 @@ def test_serving_steps(kv_gpu, name):
             for h in range(H):
                 kh = oq.dequantize(*oq.quantize(c.k[s][:n, h], "q8_0"), "q8_0")
                 vh = oq.dequantize(*oq.quantize(c.v[s][:n, h], "q4_0"), "q4_0")
-                ref = attend_rows(qx[s, h * group:(h + 1) * group], kh, vh, np.ones((group, n), bool))
+                ref = attend_rows(qx[s, h * group:(h + 1) * group], kh, vh, np.ones((group, n), bool),
+                                  *(x[:n] for x in c.codes(s, h)))
                 check_attention(o[s, h * group:(h + 1) * group], l[s, h * group:(h + 1) * group], *ref, n, name)
         pos += 1
     # the bytes are those of the single-sequence writer
@@ -517,6 +508,7 @@ def test_offsets_past_32_bits(kv_gpu):
         # a row's window reaches the row before it; position 253, before the first, holds zeros
         keys = np.concatenate([np.zeros((1 if i == 0 else 0, 256)), back[lo:i + 1, 0].cpu().numpy()])
         vals = np.concatenate([np.zeros((1 if i == 0 else 0, 256)), vback[lo:i + 1, 0].cpu().numpy()])
-        ref = attend_rows(q[i].cpu().numpy(), keys, vals, np.ones((6, 2), bool))
+        ref = attend_rows(q[i].cpu().numpy(), keys, vals, np.ones((6, 2), bool), np.full((2, 256), 8),
+                          np.abs(vals).max(1, keepdims=True) / 8)
         check_attention(out[i].cpu().numpy(), lse[i].cpu().numpy(), *ref, 2, "float32")
     assert kv.kvattn_device_error() == 0
