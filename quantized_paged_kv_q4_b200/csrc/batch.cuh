@@ -27,17 +27,34 @@ struct BatchParams {
   int n_seqs, max_rows, max_blocks, n_kv;
 };
 
-// Eight consecutive elements of a row as fp32 (exact).
+// Eight consecutive elements of a row, as they are loaded ...
 template <typename T>
-__device__ __forceinline__ void load8(const void* data, long long at, float (&x)[8]) {
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const void* data, long long at) {
+  const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(data) + at);
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.v[i] = s[i];
+  return r;
+}
+
+// ... and as fp32 (exact).
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&x)[8]) {
   if constexpr (sizeof(T) == 4) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(data) + at);
-    const float4 a = s[0], b = s[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[4 * i] = __uint_as_float(r.v[i].x);
+      x[4 * i + 1] = __uint_as_float(r.v[i].y);
+      x[4 * i + 2] = __uint_as_float(r.v[i].z);
+      x[4 * i + 3] = __uint_as_float(r.v[i].w);
+    }
   } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const T*>(data) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (std::is_same_v<T, __half>) {
@@ -49,6 +66,11 @@ __device__ __forceinline__ void load8(const void* data, long long at, float (&x)
       }
     }
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const void* data, long long at, float (&x)[8]) {
+  widen8<T>(load_raw8<T>(data, at), x);
 }
 
 // Two fp32 -> two 16-bit elements in one word (lo in the low half), round to nearest.

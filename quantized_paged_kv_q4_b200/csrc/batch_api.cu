@@ -63,11 +63,11 @@ BatchParams params_of(const kvattn_kv_desc* d, const kvattn_batch* b) {
   return p;
 }
 
-// The workspace of a decode: the plan's header, the first tile of every unit, two partials per CTA.
+// The workspace of a decode: where every unit's partials are, and two partials per CTA.
 struct BatchPlan {
   int sms;
   long long most_tiles;  // of all units together
-  size_t start_off, lse_off, o_off, bytes;
+  size_t lse_off, o_off, bytes;
 };
 
 BatchPlan plan_batch(const kvattn_kv_desc* d, const kvattn_batch* b) {
@@ -77,8 +77,7 @@ BatchPlan plan_batch(const kvattn_kv_desc* d, const kvattn_batch* b) {
   p.most_tiles = units * 8 * std::max(b->max_blocks, 1);
   const int row_tiles = batch_row_tiles(d->n_q_heads / d->n_kv_heads * std::max(b->max_rows, 1));
   const size_t slots = static_cast<size_t>(batch_grid_bound(p.sms, row_tiles)) * 2 * row_tiles * 8;
-  p.start_off = 256;
-  p.lse_off = round_up(p.start_off + sizeof(long long) * units, 256);
+  p.lse_off = round_up(sizeof(int2) * std::max(units, 1ll), 256);
   p.o_off = round_up(p.lse_off + sizeof(float) * slots, 256);
   p.bytes = p.o_off + sizeof(float) * slots * kHeadDim;
   return p;
@@ -165,8 +164,7 @@ KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batc
   p.group = group;
   p.window = window;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  p.share = reinterpret_cast<long long*>(w);
-  p.unit_start = reinterpret_cast<long long*>(w + plan.start_off);
+  p.unit_parts = reinterpret_cast<int2*>(w);
   p.part_lse = reinterpret_cast<float*>(w + plan.lse_off);
   p.part_o = reinterpret_cast<float*>(w + plan.o_off);
   const cudaError_t e = launch_decode_batch(p, q->dtype, key_format_id(desc->k_fmt), value_format_id(desc->v_fmt),

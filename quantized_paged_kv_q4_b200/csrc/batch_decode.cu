@@ -3,10 +3,11 @@
 // tokens and verify batches).
 //
 // A unit is one (sequence, KV head): its query rows (group x rows <= 24) against its 16-token
-// tiles.  All units' tiles form one line, and every CTA takes an equal stretch of it, whatever
-// the lengths are: a CTA may hold the end of one unit, some whole ones and the start of another.
-// The stretch is found on the device, because the lengths live there: every CTA adds up the
-// tiles of all sequences (one or a few per thread, then a scan) and looks its start up.
+// tiles.  All units form one line, each as long as its tiles and what a unit costs beside them
+// (kUnitCost), and every CTA takes an equal stretch of it, whatever the lengths are: a CTA may
+// hold the end of one unit, some whole ones and the start of another.  The stretch is found on
+// the device, because the lengths live there: every CTA adds up all sequences (one or a few per
+// thread, then a scan) and looks its ends up.
 //
 // Inside a CTA the warps of a group share each tile, one warp per 8 query rows; the groups take
 // the CTA's tiles in turn.  A group streams its own tiles through a ring of stages with bulk
@@ -33,9 +34,8 @@ struct BatchDecodeParams {
   const int32_t* page_logical;  // [n_seqs][n_kv][max_blocks] or null
   const int32_t* n_list;        // [n_seqs][n_kv] or null
   int group, window;
-  // workspace: the plan (tiles per CTA, then the first tile of every unit) and two partials per CTA
-  long long* share;
-  long long* unit_start;
+  // workspace: where each unit's partials are (first slot, last CTA), and two partials per CTA
+  int2* unit_parts;
   float* part_lse;  // [n_ctas][2][rows_pad], base 2
   float* part_o;    // [n_ctas][2][rows_pad][256]
 };
@@ -47,6 +47,27 @@ template <typename T>
 struct BatchParts {
   static constexpr int kQ = sizeof(T) == 4 ? 2 : 1;
   static constexpr int kP = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;
+};
+
+// One unit: its n tiles start at tile t0 of its list of pages (n = 0: a sequence without rows).
+struct BatchUnit {
+  int unit, h, r0, rows, pos0, t0, n;
+};
+
+// What a group's producer keeps between two tiles, in shared memory (registers are the tile's): the
+// unit of the next tile, where that starts in the CTA's numbering, and the positions its rows see.
+struct Producer {
+  int unit, start, t0, n, last, low;
+};
+
+// The CTA's plan and the unit at work, in shared memory.
+template <int WARPS>
+struct BatchPlanState {
+  long long tiles[WARPS], units[WARPS];  // of the warps' sequences
+  long long first_tile, end_tile;        // the CTA's tiles on the line of all tiles
+  int start;                             // first tile of the first unit, in the CTA's numbering (<= 0)
+  int abort;
+  BatchUnit unit;
 };
 
 template <int KF, int VF, int NT, typename T>
@@ -77,18 +98,10 @@ struct BatchCfg {
   static constexpr int kSharedOff = kRingBytes;
   static constexpr int kMetaOff = kSharedOff + (kSharedBytes + 15) / 16 * 16;
   static constexpr int kSmemBytes = kMetaOff + kMeta;
-  static_assert(kGroups * kStages * (8 + 8 + 4) + 256 <= kMeta, "meta");
-};
-
-// One unit: its n tiles start at tile t0 of its list of pages (n = 0: a sequence without rows).
-struct BatchUnit {
-  int s, h, r0, rows, pos0, t0, n;
-};
-
-// What a group's producer keeps between two tiles, in shared memory (registers are the tile's): the
-// unit of the next tile, where that starts in the CTA's numbering, and the positions its rows see.
-struct Producer {
-  int unit, start, t0, n, last, low;
+  static_assert(kGroups * kStages * (8 + 8 + 4) + sizeof(BatchPlanState<kWarps>) + kGroups * sizeof(Producer) <= kMeta,
+                "meta");
+  // What a unit costs beside its tiles (setup, merge, output), and the least a CTA takes, in tiles.
+  static constexpr int kUnitCost = 6, kMinShare = 8;
 };
 
 __device__ __forceinline__ int lds_int(const int* p) { return static_cast<int>(lds32(smem_u32(p))); }
@@ -112,15 +125,25 @@ __device__ __forceinline__ BatchSeq load_decode_seq(const BatchDecodeParams& p, 
 
 __device__ __forceinline__ BatchUnit load_unit(const BatchDecodeParams& p, int u) {
   BatchUnit w;
-  w.s = u / p.b.n_kv;
-  w.h = u - w.s * p.b.n_kv;
-  const BatchSeq q = load_decode_seq(p, w.s);
+  w.unit = u;
+  const int s = u / p.b.n_kv;
+  w.h = u - s * p.b.n_kv;
+  const BatchSeq q = load_decode_seq(p, s);
   w.r0 = q.r0;
   w.rows = q.rows;
   w.pos0 = q.pos0;
   w.t0 = seq_first_tile(p, q);
   w.n = unit_tiles(p, q, u);
   return w;
+}
+
+// The next unit that has tiles.  Only called where there is one: a later tile of the CTA's belongs to it.
+__device__ __forceinline__ BatchUnit next_unit(const BatchDecodeParams& p, int u) {
+  while (true) {
+    const BatchUnit w = load_unit(p, ++u);
+    if (w.n > 0) return w;
+    u = (u / p.b.n_kv + 1) * p.b.n_kv - 1;  // a sequence without rows: none of its heads has any
+  }
 }
 
 // Zeroes the V scales (and minima) of the tokens of a staged tile that lie past the sequence's
@@ -157,81 +180,80 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kMetaOff);   // [kGroups][kStages]
   uint64_t* empty = full + C::kGroups * C::kStages;                   // [kGroups][kStages] (NT > 1)
   int* st_key = reinterpret_cast<int*>(empty + C::kGroups * C::kStages);  // first position of the tile, -1: none
-  long long* s_sum = reinterpret_cast<long long*>(st_key + C::kGroups * C::kStages);  // [kWarps]
-  int* s_plan = reinterpret_cast<int*>(s_sum + C::kWarps);  // [0] abort, [1] first unit, [2] its start, [3] tiles
-  int* s_unit = s_plan + 4;                                 // [0] r0, [1] rows, [2] pos0, [3] n: the unit at work
-  Producer* prod = reinterpret_cast<Producer*>(s_unit + 4) + grp;  // the group's producer, between two tiles
+  auto* plan = reinterpret_cast<BatchPlanState<C::kWarps>*>(st_key + C::kGroups * C::kStages);
+  Producer* prod = reinterpret_cast<Producer*>(plan + 1) + grp;  // the group's, between two tiles
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kGroups * C::kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], NT);
     }
-    s_plan[0] = 0;
-    s_plan[1] = -1;
+    plan->abort = 0;
     fence_barrier_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // only now, so that the merge grid may read the batch's arrays before this grid is done
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- the plan: this CTA's stretch of the line of all units' tiles
+  // ---- the plan: this CTA's stretch of the line of all units
   {
     const int per = (p.b.n_seqs + C::kThreads - 1) / C::kThreads;
     const int s0 = min(static_cast<int>(threadIdx.x) * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
-    long long mine = 0;
+    long long tiles = 0, units = 0;  // of this thread's sequences
     for (int s = s0; s < s1; ++s) {
       const BatchSeq q = load_decode_seq(p, s);
+      if (q.rows == 0) continue;
       const long long u = static_cast<long long>(s) * p.b.n_kv;
+      units += p.b.n_kv;
       if (p.n_list)
-        for (int h = 0; h < p.b.n_kv; ++h) mine += unit_tiles(p, q, u + h);
+        for (int h = 0; h < p.b.n_kv; ++h) tiles += unit_tiles(p, q, u + h);
       else
-        mine += static_cast<long long>(p.b.n_kv) * unit_tiles(p, q, u);
+        tiles += static_cast<long long>(p.b.n_kv) * unit_tiles(p, q, u);
     }
-    long long before = mine;
+    long long t_end = tiles, u_end = units;  // inclusive sums over the warp, then the block
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, before, d);
-      if (lane >= d) before += v;
+      const long long a = __shfl_up_sync(0xffffffffu, t_end, d), b = __shfl_up_sync(0xffffffffu, u_end, d);
+      if (lane >= d) t_end += a, u_end += b;
     }
-    if (lane == 31) s_sum[warp] = before;
-    before -= mine;
+    if (lane == 31) plan->tiles[warp] = t_end, plan->units[warp] = u_end;
     __syncthreads();
-    long long total = 0;
+    long long t_all = 0, u_all = 0;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      if (w < warp) before += s_sum[w];
-      total += s_sum[w];
+      if (w < warp) t_end += plan->tiles[w], u_end += plan->units[w];
+      t_all += plan->tiles[w], u_all += plan->units[w];
     }
-    // at least kMinTiles per CTA: below that a merge costs more than the tiles it spreads
-    constexpr int kMinTiles = 2 * C::kGroups;
-    const long long share = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinTiles));
-    const long long f0 = share * blockIdx.x;
-    __syncthreads();                          // every thread has read s_sum
-    if (threadIdx.x == 0) s_sum[0] = share;  // kept: the start of a unit on the line
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.share = share;
-    if (f0 >= before && f0 < before + mine) {  // one thread of the block: the sequence of f0 is its own
-      for (int s = s0; s < s1; ++s) {
+    const long long all = t_all + C::kUnitCost * u_all;
+    const long long share = max((all + gridDim.x - 1) / gridDim.x, static_cast<long long>(C::kMinShare));
+    const long long w0 = share * blockIdx.x, w1 = min(w0 + share, all);
+    if (w0 >= all) return;  // past the end of the line
+    // the threads whose sequences hold the two ends
+    const long long at1 = t_end + C::kUnitCost * u_end, at0 = at1 - tiles - C::kUnitCost * units;
+    const bool has0 = w0 >= at0 && w0 < at1, has1 = w1 > at0 && w1 <= at1;
+    if (has0 || has1) {
+      long long at = at0, before = t_end - tiles;  // where the unit starts, and the tiles before it
+      for (int s = s0; s < s1 && at < w1; ++s) {
         const BatchSeq q = load_decode_seq(p, s);
-        bool found = false;
-        for (int h = 0; h < p.b.n_kv && !found; ++h) {
-          const long long u = static_cast<long long>(s) * p.b.n_kv + h;
-          const int n = unit_tiles(p, q, u);
-          if (f0 < before + n) {
-            s_plan[1] = static_cast<int>(u);
-            s_plan[2] = static_cast<int>(before - f0);
-            s_plan[3] = static_cast<int>(min(share, total - f0));
-            found = true;
-          } else {
-            before += n;
+        for (int h = 0; h < p.b.n_kv && q.rows > 0 && at < w1; ++h) {
+          const int u = s * p.b.n_kv + h, n = unit_tiles(p, q, u);
+          const long long first = at + C::kUnitCost, end = first + n;
+          if (has0 && w0 >= at && w0 < end) {
+            const int skip = static_cast<int>(max(w0 - first, 0ll));
+            plan->first_tile = before + skip;
+            plan->start = -skip;
+            plan->unit = BatchUnit{u, h, q.r0, q.rows, q.pos0, seq_first_tile(p, q), n};
           }
+          if (has1 && w1 > at && w1 <= end) plan->end_tile = before + max(w1 - first, 0ll);
+          at = end;
+          before += n;
         }
-        if (found) break;
       }
     }
     __syncthreads();
   }
-  if (s_plan[1] < 0) return;  // past the end of the line
-  const int n_tiles = s_plan[3];
+  const int n_tiles = static_cast<int>(plan->end_tile - plan->first_tile);
+  if (n_tiles == 0) return;  // nothing but the cost of a unit
 
   // ---- the group's ring.  Tiles are numbered along the CTA's stretch; group grp takes tiles k with
   // k % kGroups == grp, its j-th being k = grp + j kGroups in stage j % kStages.  The producer is
@@ -253,17 +275,18 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
       region = F::v_reg_off(r) / 256 | F::v_reg_tile(r) / 256 << 8 | (L::kKBytes + L::v_off(r)) / 256 << 16;
 
   int p_page = -1, p_block = -1;  // page and logical block of the next tile to issue, loaded a tile ahead
-  auto start_unit = [&](int u, int start) {
-    const BatchUnit w = load_unit(p, u);
-    if (lane == 0) {
-      prod->unit = u;
-      prod->start = start;
-      prod->t0 = w.t0;
-      prod->n = w.n;
-      prod->last = w.pos0 + w.rows - 1;
-      prod->low = p.window > 0 ? max(0, w.pos0 - p.window + 1) : 0;
-    }
+  auto start_unit = [&](const BatchUnit& w, int start) {
+    if (lane == 0)
+      *prod = Producer{w.unit, start, w.t0, w.n, w.pos0 + w.rows - 1, p.window > 0 ? max(0, w.pos0 - p.window + 1) : 0};
     __syncwarp();
+  };
+  // page and logical block of tile k of the producer's unit
+  auto page_of = [&](int k) -> int2 {
+    const int u = lds_int(&prod->unit);
+    const int i = (lds_int(&prod->t0) + k - lds_int(&prod->start)) >> 3;
+    const long long at = static_cast<long long>(u) * p.b.max_blocks + i;
+    const bool any = i < p.b.max_blocks && (!p.n_list || i < p.n_list[u]);
+    return make_int2(any ? p.b.page_table[at] : -2, any && p.page_logical ? p.page_logical[at] : i);
   };
   // looks up the page of the group's tile jj (the issue that follows uses it, a tile's arithmetic later)
   auto look_up = [&](int jj) {
@@ -272,18 +295,13 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
     while (true) {
       const int end = lds_int(&prod->start) + lds_int(&prod->n);
       if (k < end) break;
-      // a sequence without rows has no tile: on to the next one
       const int u = lds_int(&prod->unit);
-      const int next = lds_int(&prod->n) == 0 ? (u / p.b.n_kv + 1) * p.b.n_kv : u + 1;
       __syncwarp();
-      start_unit(next, end);
+      start_unit(next_unit(p, u), end);
     }
-    const int u = lds_int(&prod->unit);
-    const int i = (lds_int(&prod->t0) + k - lds_int(&prod->start)) >> 3;
-    const long long at = static_cast<long long>(u) * p.b.max_blocks + i;
-    const bool any = i < p.b.max_blocks && (!p.n_list || i < p.n_list[u]);
-    p_page = any ? p.b.page_table[at] : -2;
-    p_block = any && p.page_logical ? p.page_logical[at] : i;
+    const int2 at = page_of(k);
+    p_page = at.x;
+    p_block = at.y;
   };
   // copies the group's tile jj into its stage
   auto issue = [&](int jj) {
@@ -315,51 +333,53 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
                &gfull[st]);
     }
   };
-  if (nt0 == 0) {
-    start_unit(s_plan[1], s_plan[2]);
-    for (int jj = 0; jj < C::kStages; ++jj) {
-      look_up(jj);
-      issue(jj);
-    }
-    look_up(C::kStages);
-  }
-
   int j = 0;  // tiles this group has consumed
-  int unit = s_plan[1], start = s_plan[2];
+  int start = plan->start;
   const uint32_t q_s = smem_u32(smem + C::kSharedOff);
   bool ok = true;
+  if (nt0 == 0) start_unit(plan->unit, start);
 
   for (int done = 0; done < n_tiles;) {
-    const BatchUnit un = load_unit(p, unit);
-    if (un.n == 0) {  // a sequence without rows
-      unit = (un.s + 1) * p.b.n_kv;
-      continue;
-    }
+    const BatchUnit un = plan->unit;
     const int end = min(start + un.n, n_tiles);  // this CTA's tiles of the unit: [done, end)
-    if (threadIdx.x == 0) {
-      s_unit[0] = un.r0;
-      s_unit[1] = un.rows;
-      s_unit[2] = un.h;
-      s_unit[3] = un.n;
-    }
 
     // ---- the query's fragments.  A row is scaled by the power of two that puts its largest
     // magnitude into [1, 2) (exact), and split into f16 parts.
     float crow[2];
     uint32_t qsb_hi = 0u, qsb_lo = 0u;
     {
+      // every load before any use: the pages of the ring's first tiles (lane jj the group's tile
+      // jj), then the query rows
+      int2 ahead = make_int2(-2, 0);
+      const int k_ahead = grp + lane * C::kGroups;
+      if (done == 0 && nt0 == 0 && lane < C::kStages && k_ahead < end) ahead = page_of(k_ahead);
       const int r = nt0 * 8 + g;
-      float x[kBlocks][8];
-      if (r < un.rows * p.group) {
+      Raw8<T> raw[kBlocks];
+      const bool live = r < un.rows * p.group;
+      if (live) {
         const int qi = r / p.group, jj = r - qi * p.group;
         const long long at = (un.r0 + qi) * p.q.row_stride + (un.h * p.group + jj) * p.q.head_stride;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) load8<T>(p.q.data, at + 32 * b + 8 * t, x[b]);
-      } else {
+        for (int b = 0; b < kBlocks; ++b) raw[b] = load_raw8<T>(p.q.data, at + 32 * b + 8 * t);
+      }
+      if (done == 0 && nt0 == 0) {
+        for (int jj = 0; jj < C::kStages; ++jj) {
+          p_page = __shfl_sync(0xffffffffu, ahead.x, jj);
+          p_block = __shfl_sync(0xffffffffu, ahead.y, jj);
+          if (grp + jj * C::kGroups >= end) look_up(jj);  // already another unit's
+          issue(jj);
+        }
+        look_up(C::kStages);
+      }
+      float x[kBlocks][8];
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
+      for (int b = 0; b < kBlocks; ++b) {
+        if (live) {
+          widen8<T>(raw[b], x[b]);
+        } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[b][e] = 0.f;
+        }
       }
       float amax = 0.f;
 #pragma unroll
@@ -422,6 +442,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
     // ---- this group's tiles of the unit
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     float oacc[2 * kTileBlocks][4], racc[4] = {0.f, 0.f, 0.f, 0.f};
+    BatchUnit next{};  // the last warp's lane 0: the unit after this one
 #pragma unroll
     for (int i = 0; i < 2 * kTileBlocks; ++i)
 #pragma unroll
@@ -497,7 +518,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
           }
         }
     }
-    if (!ok) *reinterpret_cast<volatile int*>(&s_plan[0]) = 1;
+    if (!ok) *reinterpret_cast<volatile int*>(&plan->abort) = 1;
     float4* slots = reinterpret_cast<float4*>(smem + C::kSharedOff);
     constexpr int kSlot4 = C::kSlotBytes / 16;  // float4s of a slot; (m, l) behind the 16 x 32 of o
 #pragma unroll
@@ -508,6 +529,20 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
 #pragma unroll
         for (int i = 0; i < 2 * kTileBlocks; ++i) to[32 * i] = make_float4(oacc[i][0], oacc[i][1], oacc[i][2], oacc[i][3]);
         to[32 * 2 * kTileBlocks] = make_float4(m_run[0], m_run[1], l_run[0], l_run[1]);
+        // the last warp, now idle, looks up the next unit and fetches its query rows into L2
+        if (warp == C::kWarps - 1 && end < n_tiles) {
+          const BatchUnit nx = next_unit(p, un.unit);
+          if (lane < nx.rows * p.group) {
+            const int qi = lane / p.group;
+            const char* row = static_cast<const char*>(p.q.data) +
+                              sizeof(T) * ((nx.r0 + qi) * p.q.row_stride +
+                                           (nx.h * p.group + lane - qi * p.group) * p.q.head_stride);
+#pragma unroll
+            for (int b = 0; b < kHeadDim * static_cast<int>(sizeof(T)); b += 128)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(row + b));
+          }
+          if (lane == 0) next = nx;
+        }
       }
       __syncthreads();
       if (grp < half) {
@@ -535,8 +570,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
       }
     }
     __syncthreads();
-    if (s_plan[0]) break;
-    const int unit_n = lds_int(&s_unit[3]);
+    if (plan->abort) break;
     if (grp == 0) {
       // rows of 256 through the warp's slot, so that lanes store whole lines
       float* rows = reinterpret_cast<float*>(slots + nt0 * kSlot4);
@@ -552,9 +586,11 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
             rows[(2 * t + c) * C::kOStride + 16 * i + g + 8 * hi] = oacc[i][c + 2 * hi] * inv;
       }
       __syncwarp();
-      const int r0 = lds_int(&s_unit[0]), n_rows = lds_int(&s_unit[1]) * p.group, h = lds_int(&s_unit[2]);
+      const int r0 = lds_int(&plan->unit.r0), n_rows = lds_int(&plan->unit.rows) * p.group;
+      const int h = lds_int(&plan->unit.h), unit_n = lds_int(&plan->unit.n);
       const bool whole = start >= 0 && start + unit_n <= n_tiles;
-      const long long part = (static_cast<long long>(blockIdx.x) * 2 + (start <= 0 ? 0 : 1)) * C::kRowsPad;
+      const int slot = static_cast<int>(blockIdx.x) * 2 + (start <= 0 ? 0 : 1);
+      const long long part = static_cast<long long>(slot) * C::kRowsPad;
 #pragma unroll 1
       for (int r = 0; r < 8; ++r) {
         const int row = nt0 * 8 + r;
@@ -573,15 +609,21 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
           if (lane == 0) p.part_lse[part + row] = l2;
         }
       }
-      if (start >= 0 && threadIdx.x == 0)
-        p.unit_start[unit] = static_cast<long long>(blockIdx.x) * s_sum[0] + start;
+      if (threadIdx.x == 0) {
+        int2* parts = p.unit_parts + lds_int(&plan->unit.unit);
+        if (start >= 0) parts->x = slot;
+        if (start + unit_n <= n_tiles) parts->y = static_cast<int>(blockIdx.x);
+      }
     }
     done = end;
-    start += unit_n;
-    ++unit;
-    __syncthreads();  // the slots and s_unit, before the next unit's
+    start = end;
+    __syncthreads();  // the slots and the plan's unit, before the next unit's
+    if (done < n_tiles) {
+      if (warp == C::kWarps - 1 && lane == 0) plan->unit = next;
+      __syncthreads();
+    }
   }
-  if (s_plan[0] && nt0 == 0 && lane == 0) {
+  if (plan->abort && nt0 == 0 && lane == 0) {
     // a bounded wait expired: wait (bounded) for the copies still in flight, then leave
     const int issued = min(j + C::kStages, (n_tiles - grp + C::kGroups - 1) / C::kGroups);
     const unsigned long long t0 = global_timer_ns();
@@ -599,19 +641,18 @@ constexpr int kBatchMergeAhead = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(256) merge_batch_kernel(const BatchDecodeParams p, int rows_pad) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float red_m[4], red_l[4];
   __shared__ float4 red_o[4][kHeadDim / 4];
   const int u = blockIdx.x;
+  // the split grid started this one after its own wait: what came before it is there to be read
   const BatchUnit un = load_unit(p, u);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (un.n == 0) return;
-  const long long share = *p.share, start = p.unit_start[u];
-  const long long c0 = start / share, c1 = (start + un.n - 1) / share;
-  if (c0 == c1) return;  // written by its CTA
-  const int n_parts = static_cast<int>(c1 - c0) + 1;
+  const int2 parts = p.unit_parts[u];
+  const int c0 = parts.x >> 1, n_parts = parts.y - c0 + 1;
+  if (n_parts == 1) return;  // written by its CTA
   const int tid = threadIdx.x, grp = tid >> 6, d4 = tid & 63;
-  const long long first = c0 * 2 + (start == c0 * share ? 0 : 1);  // part i > 0 is slot 0 of CTA c0 + i
   for (int row = blockIdx.y; row < un.rows * p.group; row += gridDim.y) {
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -621,7 +662,7 @@ __global__ void __launch_bounds__(256) merge_batch_kernel(const BatchDecodeParam
 #pragma unroll
       for (int k = 0; k < kBatchMergeAhead; ++k) {
         const int i = i0 + 4 * k;
-        const long long at = (i == 0 ? first : 2 * (c0 + i)) * rows_pad + row;
+        const long long at = static_cast<long long>(i == 0 ? parts.x : 2 * (c0 + i)) * rows_pad + row;
         v[k] = i < n_parts ? p.part_lse[at] : -INFINITY;
         o[k] = i < n_parts ? *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + 4 * d4)
                            : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -691,7 +732,7 @@ static cudaError_t launch_batch_t(const BatchDecodeParams& p, int sms, long long
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(
-      std::min<long long>(static_cast<long long>(sms) * C::kCtas, (most_tiles + 2 * C::kGroups - 1) / (2 * C::kGroups))));
+      std::min(static_cast<long long>(sms) * C::kCtas, (most_tiles + C::kUnitCost * units) / C::kMinShare + 1)));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;

@@ -186,19 +186,31 @@ def make_desc(n_kv_heads, n_q_heads, k_pool, v_pool, n_pages, v_fmt="q4_0", k_pa
                           n_pages, sm_budget, 0)
 
 
-_DTYPES = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
+def _batch_device() -> int:
+    """The current device: the batch calls launch there, and take tensors of no other."""
+    import torch
+
+    return torch.cuda.current_device()
 
 
-def _i32(x, what, shape=None):
-    """A device int32 array of the batch calls: a contiguous CUDA tensor (its shape checked where
-    one is given), a raw address or None."""
-    if x is None or isinstance(x, int):
-        return x
-    if str(x.dtype) != "torch.int32":
-        raise ValueError(f"{what}: expected int32, got {x.dtype}")
-    if shape is not None and tuple(x.shape) != shape:
-        raise ValueError(f"{what}: expected shape {shape}, got {tuple(x.shape)}")
-    return _d(x)
+def _on(x, what, device) -> int:
+    """The address of a contiguous CUDA tensor on `device`."""
+    if x.get_device() != device:  # -1: a CPU tensor
+        raise ValueError(f"{what}: expected a CUDA tensor on the current device, cuda:{device}, got one on {x.device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return x.data_ptr()
+
+
+def _i32(x, what, device, shape):
+    """A device int32 array of the batch calls, or None."""
+    import torch
+
+    if x is None:
+        return None
+    if x.dtype is not torch.int32 or x.shape != shape:
+        raise ValueError(f"{what}: expected int32 {shape}, got {x.dtype} {tuple(x.shape)}")
+    return _on(x, what, device)
 
 
 def make_batch(row_start, pos_start, page_table, n_rows, max_rows) -> kvattn_batch:
@@ -209,37 +221,46 @@ def make_batch(row_start, pos_start, page_table, n_rows, max_rows) -> kvattn_bat
     if page_table.dim() != 3:
         raise ValueError(f"page_table: expected [n_seqs][H_kv][max_blocks], got {tuple(page_table.shape)}")
     n_seqs, heads, max_blocks = page_table.shape
-    _one_device("make_batch", row_start, pos_start, page_table)
-    b = kvattn_batch(_i32(row_start, "row_start", (n_seqs + 1,)), _i32(pos_start, "pos_start", (n_seqs,)),
-                     _i32(page_table, "page_table"), n_rows, n_seqs, max_rows, max_blocks, 0)
-    b.heads, b.device = heads, page_table.device
+    device = _batch_device()
+    b = kvattn_batch(_i32(row_start, "row_start", device, (n_seqs + 1,)),
+                     _i32(pos_start, "pos_start", device, (n_seqs,)),
+                     _i32(page_table, "page_table", device, (n_seqs, heads, max_blocks)),
+                     n_rows, n_seqs, max_rows, max_blocks, 0)
+    b.heads, b.device = heads, device
     return b
 
 
-def _one_device(what, *tensors):
-    """The batch calls launch on the current device: a tensor of another one is refused here."""
-    import torch
-
-    now = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and t.is_cuda and t.device.index != now:
-            raise ValueError(f"{what}: a tensor is on {t.device}, the current device is cuda:{now}")
+_dtypes = {}
 
 
-def make_rows(x, n_rows, heads) -> kvattn_rows:
+def make_rows(x, n_rows, heads, device=None) -> kvattn_rows:
     """A token array [n_rows][heads][256] of fp32, fp16 or bf16 as the batch calls take it: any
     strides over rows and heads (a slice of a fused projection, say), the channels contiguous."""
-    if not x.is_cuda:
-        raise ValueError(f"expected a CUDA tensor for a device-memory argument, got one on {x.device}")
-    if tuple(x.shape) != (n_rows, heads, 256):
+    if not _dtypes:
+        import torch
+
+        _dtypes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    at = x.get_device()
+    if at < 0 or at != (device if device is not None else _batch_device()):
+        raise ValueError(f"expected a CUDA tensor on the current device for a token array, got one on {x.device}")
+    if x.shape != (n_rows, heads, 256):
         raise ValueError(f"expected a token array of shape {(n_rows, heads, 256)}, got {tuple(x.shape)}")
-    dtype = _DTYPES.get(str(x.dtype))
+    dtype = _dtypes.get(x.dtype)
     if dtype is None:
         raise ValueError(f"expected float32, float16 or bfloat16, got {x.dtype}")
     rs, hs, cs = x.stride()
     if cs != 1:
         raise ValueError("expected contiguous channels (the last stride must be 1)")
     return kvattn_rows(x.data_ptr(), rs, hs, dtype, 0)
+
+
+def _batch_stream(stream, device):
+    """As _s, with the current stream's handle taken directly (the Stream object costs 4 us a call)."""
+    if stream is None:
+        import torch
+
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _s(stream)
 
 
 # ---------------------------------------------------------------- entry points
@@ -385,29 +406,33 @@ def kvattn_resident_update(sel_logical, n_sel, cap, n_units, n_blocks, n_full, s
            "kvattn_resident_update")
 
 
-def _check_batch(what, desc, batch, *tensors):
+def _check_batch(what, desc, batch) -> int:
+    """The device of a batch call: the batch's, which has to be the current one."""
     if batch.heads != desc.n_kv_heads:
         raise ValueError(f"{what}: page_table has {batch.heads} KV heads, the descriptor {desc.n_kv_heads}")
-    for t in tensors:
-        if t is not None and t.device != batch.device:
-            raise ValueError(f"{what}: a tensor is on {t.device}, the batch on {batch.device}")
-    _one_device(what, *tensors)
+    device = batch.device
+    if device != _batch_device():
+        raise ValueError(f"{what}: the batch is on cuda:{device}, the current device is cuda:{_batch_device()}")
+    return device
 
 
 def kvattn_append_batch(desc, batch, k, v, stream=None) -> None:
     """Quantize-append every row of the batch into its page; k, v [n_rows][H_kv][256], of one of the
     three types, with any strides over rows and heads."""
-    _check_batch("kvattn_append_batch", desc, batch, k, v)
-    kr, vr = (make_rows(x, batch.n_rows, desc.n_kv_heads) for x in (k, v))
-    _check(lib().kvattn_append_batch(desc, batch, kr, vr, _s(stream)), "kvattn_append_batch")
+    device = _check_batch("kvattn_append_batch", desc, batch)
+    n, heads = batch.n_rows, batch.heads
+    _check(lib().kvattn_append_batch(desc, batch, make_rows(k, n, heads, device), make_rows(v, n, heads, device),
+                                     _batch_stream(stream, device)), "kvattn_append_batch")
 
 
 def kvattn_read_batch(desc, batch, k=None, v=None, stream=None) -> None:
     """The values that the cache holds for every row of the batch, into k and / or v
     [n_rows][H_kv][256] (rows of no sequence are left as they were)."""
-    _check_batch("kvattn_read_batch", desc, batch, k, v)
-    kr, vr = (None if x is None else make_rows(x, batch.n_rows, desc.n_kv_heads) for x in (k, v))
-    _check(lib().kvattn_read_batch(desc, batch, kr, vr, _s(stream)), "kvattn_read_batch")
+    device = _check_batch("kvattn_read_batch", desc, batch)
+    n, heads = batch.n_rows, batch.heads
+    _check(lib().kvattn_read_batch(desc, batch, None if k is None else make_rows(k, n, heads, device),
+                                   None if v is None else make_rows(v, n, heads, device),
+                                   _batch_stream(stream, device)), "kvattn_read_batch")
 
 
 def kvattn_decode_batch_workspace_size(desc, batch) -> int:
@@ -416,15 +441,19 @@ def kvattn_decode_batch_workspace_size(desc, batch) -> int:
 
 def kvattn_decode_batch(desc, batch, q, out, lse, ws, page_logical=None, n_pages=None, window=0, stream=None) -> None:
     """Attention of every row of the batch over its sequence's pages: q, out [n_rows][H_q][256] of one
-    type, lse fp32 [n_rows][H_q], ws a uint8 tensor of kvattn_decode_batch_workspace_size bytes."""
-    _check_batch("kvattn_decode_batch", desc, batch, q, out, lse, ws, page_logical, n_pages)
-    qr, outr = (make_rows(x, batch.n_rows, desc.n_q_heads) for x in (q, out))
-    if str(lse.dtype) != "torch.float32" or tuple(lse.shape) != (batch.n_rows, desc.n_q_heads):
-        raise ValueError(f"lse: expected float32 {(batch.n_rows, desc.n_q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
-    lists = (batch.n_seqs, batch.heads, batch.max_blocks)
-    _check(lib().kvattn_decode_batch(desc, batch, qr, _i32(page_logical, "page_logical", lists),
-                                     _i32(n_pages, "n_pages", lists[:2]), window, outr, _d(lse), _d(ws),
-                                     ws.numel() * ws.element_size(), _s(stream)), "kvattn_decode_batch")
+    type, lse fp32 [n_rows][H_q], ws a tensor of at least kvattn_decode_batch_workspace_size bytes."""
+    import torch
+
+    device = _check_batch("kvattn_decode_batch", desc, batch)
+    n, heads, q_heads = batch.n_rows, batch.heads, desc.n_q_heads
+    if lse.dtype is not torch.float32 or lse.shape != (n, q_heads):
+        raise ValueError(f"lse: expected float32 {(n, q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
+    _check(lib().kvattn_decode_batch(desc, batch, make_rows(q, n, q_heads, device),
+                                     _i32(page_logical, "page_logical", device, (batch.n_seqs, heads, batch.max_blocks)),
+                                     _i32(n_pages, "n_pages", device, (batch.n_seqs, heads)), window,
+                                     make_rows(out, n, q_heads, device), _on(lse, "lse", device),
+                                     _on(ws, "ws", device), ws.nbytes, _batch_stream(stream, device)),
+           "kvattn_decode_batch")
 
 
 def _host_i32(a):

@@ -140,17 +140,29 @@ def test_binding_checks_tensors():
 
     x = torch.zeros((3, 4, 256))
     with pytest.raises(ValueError, match="CUDA"):
-        kvattn.make_rows(x, 3, 4)
-    fake = type("T", (), {"is_cuda": True, "shape": (3, 4, 256), "dtype": torch.float64, "stride": lambda s: (1024, 256, 1)})
+        kvattn.make_rows(x, 3, 4, 0)
+    fake = type("T", (), {"shape": (3, 4, 256), "dtype": torch.float64, "device": "cuda:1",
+                          "get_device": lambda s: 1, "stride": lambda s: (1024, 256, 1)})
+    with pytest.raises(ValueError, match="current device"):
+        kvattn.make_rows(fake(), 3, 4, 0)
     with pytest.raises(ValueError, match="float32, float16 or bfloat16"):
-        kvattn.make_rows(fake(), 3, 4)
+        kvattn.make_rows(fake(), 3, 4, 1)
     with pytest.raises(ValueError, match="shape"):
-        kvattn.make_rows(fake(), 3, 5)
+        kvattn.make_rows(fake(), 3, 5, 1)
     fake.dtype, fake.stride = torch.float32, lambda s: (1024, 1, 4)
     with pytest.raises(ValueError, match="contiguous"):
-        kvattn.make_rows(fake(), 3, 4)
+        kvattn.make_rows(fake(), 3, 4, 1)
     with pytest.raises(ValueError, match="n_seqs"):
         kvattn.make_batch(x, x, x[0], 1, 1)
+    i = torch.zeros((3, 4), dtype=torch.int32)
+    for bad, match in ((i.long(), "int32"), (i[:2], "int32"), (i, "CUDA")):
+        with pytest.raises(ValueError, match=match):
+            kvattn._i32(bad, "n_pages", 0, (3, 4))
+    assert kvattn._i32(None, "n_pages", 0, (3, 4)) is None
+    b = batch()
+    b.heads, b.device = 3, 0
+    with pytest.raises(ValueError, match="KV heads"):
+        kvattn.kvattn_read_batch(desc(), b)
 
 
 @pytest.mark.parametrize("role,fmt", sorted({("k", k) for k, _ in PAIRS} | {("v", v) for _, v in PAIRS}))
