@@ -494,8 +494,9 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
  *                out = 0)
  *   ws           device workspace of kvattn_decode_batch_workspace_size() bytes, 256-byte
  *                aligned; needs no initialisation.  Calls that share one must not overlap.
- * Supports group * max_rows <= 24.  Results do not depend on the SM's timing: the split of
- * the work depends on the lengths and the device alone. */
+ * Supports group * max_rows <= 24 and n_seqs * H_kv * max_blocks <= 2^27 (table entries).
+ * Results do not depend on timing: the split of the work depends on the lengths and the device
+ * alone. */
 KVATTN_API size_t kvattn_decode_batch_workspace_size(const kvattn_kv_desc* desc, const kvattn_batch* batch);
 KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batch* batch, const kvattn_rows* q,
                                    const int32_t* page_logical, const int32_t* n_pages, int32_t window,

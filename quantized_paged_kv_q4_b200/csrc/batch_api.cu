@@ -63,7 +63,7 @@ BatchParams params_of(const kvattn_kv_desc* d, const kvattn_batch* b) {
   return p;
 }
 
-// The workspace of a decode: where every unit's partials are, and two partials per CTA.
+// The workspace of a decode: where every unit's partials are, and two partials per group.
 struct BatchPlan {
   int sms;
   long long most_tiles;  // of all units together
@@ -76,7 +76,7 @@ BatchPlan plan_batch(const kvattn_kv_desc* d, const kvattn_batch* b) {
   const long long units = static_cast<long long>(b->n_seqs) * d->n_kv_heads;
   p.most_tiles = units * 8 * std::max(b->max_blocks, 1);
   const int row_tiles = batch_row_tiles(d->n_q_heads / d->n_kv_heads * std::max(b->max_rows, 1));
-  const size_t slots = static_cast<size_t>(batch_grid_bound(p.sms, row_tiles)) * 2 * row_tiles * 8;
+  const size_t slots = static_cast<size_t>(batch_group_bound(p.sms, row_tiles)) * 2 * row_tiles * 8;
   p.lse_off = round_up(sizeof(int2) * std::max(units, 1ll), 256);
   p.o_off = round_up(p.lse_off + sizeof(float) * slots, 256);
   p.bytes = p.o_off + sizeof(float) * slots * kHeadDim;
@@ -149,7 +149,8 @@ KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batc
   if (q->dtype != out->dtype) return KVATTN_ERR_UNSUPPORTED_FORMAT;
   if (!lse) return KVATTN_ERR_INVALID_ARG;
   const BatchPlan plan = plan_batch(desc, batch);
-  if (plan.most_tiles > (1ll << 38)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
+  // the line of all units' tiles (and a few per unit beside them) is counted in 32 bits
+  if (plan.most_tiles > (1ll << 30)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return KVATTN_ERR_INVALID_ARG;
   if (ws_bytes < plan.bytes) return KVATTN_ERR_WORKSPACE_TOO_SMALL;
   int dev;

@@ -3,23 +3,25 @@
 // tokens and verify batches).
 //
 // A unit is one (sequence, KV head): its query rows (group x rows <= 24) against its 16-token
-// tiles.  All units form one line, each as long as its tiles and what a unit costs beside them
-// (kUnitCost), and every CTA takes an equal stretch of it, whatever the lengths are: a CTA may
-// hold the end of one unit, some whole ones and the start of another.  The stretch is found on
-// the device, because the lengths live there: every CTA adds up all sequences (one or a few per
-// thread, then a scan) and looks its ends up.
+// tiles.  A warp group (one warp per 8 query rows) works by itself: it streams its own tiles
+// through its own ring of stages, keeps its own softmax state and writes its own results.  No
+// group waits for another, so what a unit costs beside its tiles (query fragments, output) hides
+// behind the arithmetic of the SM's other groups, and the ring runs on from one unit into the
+// next.  The copies are 16 bytes a lane (cp.async): a tile has four to six short regions, and a
+// bulk copy of each, issued by the warp that also computes, took 700 of the 3,400 cycles a tile.
 //
-// Inside a CTA the warps of a group share each tile, one warp per 8 query rows; the groups take
-// the CTA's tiles in turn.  A group streams its own tiles through a ring of stages with bulk
-// async copies (one per region of the tile; lane r copies region r), and the ring runs on across
-// units, so the next unit's first tiles arrive while the last unit's partial results are merged.
-// Two or three CTAs share an SM, so that one CTA's merge and setup hide behind the others'
-// arithmetic.  A tile's arithmetic is attend_tile (decode_tile.cuh).
+// All units form one line, each as long as its tiles and what it costs beside them (kUnitCost),
+// and every group takes an equal stretch of it, whatever the lengths are: a group may hold the end
+// of one unit, some whole ones and the start of another.  The stretches are found on the device,
+// because the lengths live there: every CTA adds up all sequences (one or a few per thread, then a
+// scan) and looks its groups' ends up.  A unit inside one group's stretch is written to out at
+// once; otherwise each of its groups leaves an (o, lse) partial and a second grid merges them, in
+// a fixed order.  A group has at most two partials, its first unit's and its last's, so the
+// workspace has two slots per group.
 //
-// At the end of a unit the groups' states (m, l, o) are merged through shared memory, pairwise,
-// in a fixed order.  A unit inside one CTA is written to out at once; otherwise each CTA leaves
-// an (o, lse) partial and a second grid merges them.  A CTA has at most two such partials, its
-// first unit's and its last's, so the workspace has two slots per CTA.
+// An earlier arrangement gave a CTA of four groups one stretch and merged the groups' states
+// through shared memory at the end of each unit: 2 to 4 us of barriers per unit (32 ragged
+// sequences of up to 16,384 tokens: 51.9 us).
 #include <algorithm>
 
 #include "batch.cuh"
@@ -34,10 +36,10 @@ struct BatchDecodeParams {
   const int32_t* page_logical;  // [n_seqs][n_kv][max_blocks] or null
   const int32_t* n_list;        // [n_seqs][n_kv] or null
   int group, window;
-  // workspace: where each unit's partials are (first slot, last CTA), and two partials per CTA
+  // workspace: where each unit's partials are (first slot, last group), and two partials per group
   int2* unit_parts;
-  float* part_lse;  // [n_ctas][2][rows_pad], base 2
-  float* part_o;    // [n_ctas][2][rows_pad][256]
+  float* part_lse;  // [groups][2][rows_pad], base 2
+  float* part_o;    // [groups][2][rows_pad][256]
 };
 
 // 16-bit inputs are exact as one f16 part (bf16's 8 bits after scaling by a power of two); fp32
@@ -54,20 +56,24 @@ struct BatchUnit {
   int unit, h, r0, rows, pos0, t0, n;
 };
 
-// What a group's producer keeps between two tiles, in shared memory (registers are the tile's): the
-// unit of the next tile, where that starts in the CTA's numbering, and the positions its rows see.
-struct Producer {
-  int unit, start, t0, n, last, low;
+// What a warp's copying keeps between two tiles, in shared memory (registers are the tile's): the
+// unit of the next tile, where that starts in the group's numbering, the positions its rows see,
+// and the page at hand: its first position (-1: nothing of it is fetched) and its bytes.
+struct alignas(16) Producer {
+  int unit, start, t0, n;
+  int last, low, key0, pad;
+  const uint8_t *k, *v;
 };
 
-// The CTA's plan and the unit at work, in shared memory.
-template <int WARPS>
-struct BatchPlanState {
-  long long tiles[WARPS], units[WARPS];  // of the warps' sequences
-  long long first_tile, end_tile;        // the CTA's tiles on the line of all tiles
-  int start;                             // first tile of the first unit, in the CTA's numbering (<= 0)
-  int abort;
-  BatchUnit unit;
+// The CTA's plan, in shared memory.
+template <int WARPS, int GROUPS>
+struct alignas(16) BatchPlanState {
+  int tiles[WARPS], units[WARPS];        // of the warps' sequences
+  int from[GROUPS], to[GROUPS];          // the groups' ends on the line of all tiles
+  BatchUnit unit[GROUPS];                // each group's first unit ...
+  int skip[GROUPS];                      // ... and its tiles that come before the group's
+  BatchUnit at_work[WARPS];              // each warp's unit (not in registers while the tiles run)
+  Producer producer[WARPS];
 };
 
 template <int KF, int VF, int NT, typename T>
@@ -75,33 +81,28 @@ struct BatchCfg {
   using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
   static constexpr int kRowsPad = NT * 8;
-  static constexpr int kWarps = NT == 3 ? 6 : 4;
-  static constexpr int kThreads = kWarps * 32;
-  static constexpr int kGroups = kWarps / NT;
-  static constexpr int kTileBytes = L::kKBytes + L::kVBytes;
-  static constexpr int kRegions = F::kKRegions + F::kVRegions;
-  // the query's B fragments, and in the same place (never at the same time) the merge slots
+  static constexpr int kTileBytes = L::kBytes;
+  // the query's B fragments: [n-tile][block][k-step][lane]
   static constexpr int kQFragBytes = BatchParts<T>::kQ == 2 ? 16 : 8;
-  static constexpr int kQBytes = 16 * NT * 32 * kQFragBytes;
-  static constexpr int kOStride = kHeadDim + 4;       // floats; rows 2t of a quad fall in different banks
-  static constexpr int kSlotBytes = 8 * kOStride * 4 + 32 * 16;  // one warp's o, then its (m, l)
-  static constexpr int kSlots = kGroups == 4 ? 2 : NT;
-  static constexpr int kSharedBytes = kQBytes > kSlots * kSlotBytes ? kQBytes : kSlots * kSlotBytes;
-  static constexpr int kMeta = 512;                   // barriers and tags
-  static constexpr int budget(int ctas) { return 228 * 1024 / ctas - 1024 - kSharedBytes - kMeta; }
-  static constexpr int kStages3 = budget(3) / (kGroups * kTileBytes);
-  static constexpr int kCtas = NT < 3 && kStages3 >= 2 ? 3 : 2;  // per SM
-  static constexpr int kStagesFit = budget(kCtas) / (kGroups * kTileBytes);
+  static constexpr int kQWarpBytes = 16 * 32 * kQFragBytes;
+  static constexpr int kMeta = 3 * 1024;  // the plan and the tiles' positions
+  // One CTA per SM, of as many groups as shared memory holds with two stages each, up to twelve
+  // warps (three per scheduler, 168 registers a thread); then as many stages as fit, up to 6.
+  static constexpr int kRoom = 227 * 1024 - kMeta;
+  static constexpr int kFit = kRoom / (NT * kQWarpBytes + 2 * kTileBytes);
+  static constexpr int kGroups = kFit < 12 / NT ? kFit : 12 / NT;
+  static constexpr int kStagesFit = (kRoom / kGroups - NT * kQWarpBytes) / kTileBytes;
   static constexpr int kStages = kStagesFit < 6 ? kStagesFit : 6;
-  static_assert(kStages >= 2, "ring");
-  static constexpr int kRingBytes = kGroups * kStages * kTileBytes;
-  static constexpr int kSharedOff = kRingBytes;
-  static constexpr int kMetaOff = kSharedOff + (kSharedBytes + 15) / 16 * 16;
+  static constexpr int kWarps = kGroups * NT;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kQOff = kGroups * kStages * kTileBytes;
+  static constexpr int kMetaOff = kQOff + kWarps * kQWarpBytes;
   static constexpr int kSmemBytes = kMetaOff + kMeta;
-  static_assert(kGroups * kStages * (8 + 8 + 4) + sizeof(BatchPlanState<kWarps>) + kGroups * sizeof(Producer) <= kMeta,
-                "meta");
-  // What a unit costs beside its tiles (setup, merge, output), and the least a CTA takes, in tiles.
-  static constexpr int kUnitCost = 6, kMinShare = 8;
+  static_assert(kStages >= 2 && kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kMeta, "meta");
+  static_assert(kMetaOff % 16 == 0 && kQOff % 16 == 0 && sizeof(BatchPlanState<kWarps, kGroups>) % 16 == 0, "alignment");
+  // What a unit costs beside its tiles, and the least a group takes, in tiles.
+  static constexpr int kUnitCost = 2, kMinShare = 4;
 };
 
 __device__ __forceinline__ int lds_int(const int* p) { return static_cast<int>(lds32(smem_u32(p))); }
@@ -161,14 +162,21 @@ __device__ __noinline__ void blank_tokens(uint8_t* vscale, uint8_t* vmin, int la
     uint2* m = reinterpret_cast<uint2*>(vmin) + lane;
     *m = make_uint2(m->x & keep[0], m->y & keep[1]);
   }
-  // the stage is later refilled by the copy engine (async proxy)
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
 }
 
+__device__ __forceinline__ const uint8_t* lds_ptr(const uint8_t* const* p) {
+  unsigned long long v;
+  asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(smem_u32(p)));
+  return reinterpret_cast<const uint8_t*>(v);
+}
+
+__device__ __forceinline__ void cp16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
 template <int KF, int VF, int NT, typename T>
-__global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF, VF, NT, T>::kCtas)
-    decode_batch_kernel(const BatchDecodeParams p) {
+__global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_batch_kernel(const BatchDecodeParams p) {
   using C = BatchCfg<KF, VF, NT, T>;
   using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
@@ -177,182 +185,211 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int grp = warp / NT, nt0 = warp % NT;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kMetaOff);   // [kGroups][kStages]
-  uint64_t* empty = full + C::kGroups * C::kStages;                   // [kGroups][kStages] (NT > 1)
-  int* st_key = reinterpret_cast<int*>(empty + C::kGroups * C::kStages);  // first position of the tile, -1: none
-  auto* plan = reinterpret_cast<BatchPlanState<C::kWarps>*>(st_key + C::kGroups * C::kStages);
-  Producer* prod = reinterpret_cast<Producer*>(plan + 1) + grp;  // the group's, between two tiles
+  auto* plan = reinterpret_cast<BatchPlanState<C::kWarps, C::kGroups>*>(smem + C::kMetaOff);
+  // first position of the tile in each of the warp's stages, -1: none
+  int* key_of = reinterpret_cast<int*>(plan + 1) + warp * C::kStages;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kGroups * C::kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], NT);
-    }
-    plan->abort = 0;
-    fence_barrier_init();
-  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // only now, so that the merge grid may read the batch's arrays before this grid is done
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- the plan: this CTA's stretch of the line of all units
+  // ---- the plan: the groups' stretches of the line of all units
   {
     const int per = (p.b.n_seqs + C::kThreads - 1) / C::kThreads;
     const int s0 = min(static_cast<int>(threadIdx.x) * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
-    long long tiles = 0, units = 0;  // of this thread's sequences
+    int tiles = 0, units = 0;  // of this thread's sequences (the host keeps the whole line below 2^31)
+    BatchSeq seq{};            // the last of them (the only one, with few sequences)
+    int n_seq = 0;             // its tiles per unit, without n_list
     for (int s = s0; s < s1; ++s) {
-      const BatchSeq q = load_decode_seq(p, s);
-      if (q.rows == 0) continue;
-      const long long u = static_cast<long long>(s) * p.b.n_kv;
+      seq = load_decode_seq(p, s);
+      if (seq.rows == 0) continue;
       units += p.b.n_kv;
-      if (p.n_list)
-        for (int h = 0; h < p.b.n_kv; ++h) tiles += unit_tiles(p, q, u + h);
-      else
-        tiles += static_cast<long long>(p.b.n_kv) * unit_tiles(p, q, u);
+      if (p.n_list) {
+        for (int h = 0; h < p.b.n_kv; ++h) tiles += unit_tiles(p, seq, static_cast<long long>(s) * p.b.n_kv + h);
+      } else {
+        n_seq = unit_tiles(p, seq, 0);
+        tiles += p.b.n_kv * n_seq;
+      }
     }
-    long long t_end = tiles, u_end = units;  // inclusive sums over the warp, then the block
+    int t_end = tiles, u_end = units;  // inclusive sums over the warp, then the block
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long a = __shfl_up_sync(0xffffffffu, t_end, d), b = __shfl_up_sync(0xffffffffu, u_end, d);
+      const int a = __shfl_up_sync(0xffffffffu, t_end, d), b = __shfl_up_sync(0xffffffffu, u_end, d);
       if (lane >= d) t_end += a, u_end += b;
     }
     if (lane == 31) plan->tiles[warp] = t_end, plan->units[warp] = u_end;
     __syncthreads();
-    long long t_all = 0, u_all = 0;
+    int t_all = 0, u_all = 0;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
       if (w < warp) t_end += plan->tiles[w], u_end += plan->units[w];
       t_all += plan->tiles[w], u_all += plan->units[w];
     }
-    const long long all = t_all + C::kUnitCost * u_all;
-    const long long share = max((all + gridDim.x - 1) / gridDim.x, static_cast<long long>(C::kMinShare));
-    const long long w0 = share * blockIdx.x, w1 = min(w0 + share, all);
-    if (w0 >= all) return;  // past the end of the line
-    // the threads whose sequences hold the two ends
-    const long long at1 = t_end + C::kUnitCost * u_end, at0 = at1 - tiles - C::kUnitCost * units;
-    const bool has0 = w0 >= at0 && w0 < at1, has1 = w1 > at0 && w1 <= at1;
-    if (has0 || has1) {
-      long long at = at0, before = t_end - tiles;  // where the unit starts, and the tiles before it
-      for (int s = s0; s < s1 && at < w1; ++s) {
-        const BatchSeq q = load_decode_seq(p, s);
-        for (int h = 0; h < p.b.n_kv && q.rows > 0 && at < w1; ++h) {
-          const int u = s * p.b.n_kv + h, n = unit_tiles(p, q, u);
-          const long long first = at + C::kUnitCost, end = first + n;
-          if (has0 && w0 >= at && w0 < end) {
-            const int skip = static_cast<int>(max(w0 - first, 0ll));
-            plan->first_tile = before + skip;
-            plan->start = -skip;
-            plan->unit = BatchUnit{u, h, q.r0, q.rows, q.pos0, seq_first_tile(p, q), n};
+    const int all = t_all + C::kUnitCost * u_all, takers = static_cast<int>(gridDim.x) * C::kGroups;
+    const int share = max((all + takers - 1) / takers, C::kMinShare);
+    // Stretch i gridDim.x + blockIdx.x is group i's: the first ones go to different SMs.
+    const int stride = share * static_cast<int>(gridDim.x), base = share * static_cast<int>(blockIdx.x);
+    if (base >= all) return;  // past the end of the line
+    if (threadIdx.x < C::kGroups) {
+      const long long from = base + static_cast<long long>(threadIdx.x) * stride;
+      if (from >= all) plan->from[threadIdx.x] = t_all;
+      if (from + share >= all) plan->to[threadIdx.x] = t_all;
+    }
+    // Every end belongs to the thread whose sequences hold it: end e (0: a stretch's start, 1: its
+    // end) of group i sits at base + e share + i stride.
+    int at = t_end + C::kUnitCost * u_end - tiles - C::kUnitCost * units, before = t_end - tiles;
+    for (int s = s0; s < s1 && units > 0; ++s) {
+      if (per > 1) {
+        seq = load_decode_seq(p, s);
+        if (seq.rows == 0) continue;
+        if (!p.n_list) n_seq = unit_tiles(p, seq, 0);
+      }
+      // units of one length are passed in one go, units with lists one by one
+      const int step = p.n_list ? 1 : p.b.n_kv;
+      for (int h0 = 0; h0 < p.b.n_kv; h0 += step) {
+        const int n = p.n_list ? unit_tiles(p, seq, static_cast<long long>(s) * p.b.n_kv + h0) : n_seq;
+        const int len = C::kUnitCost + n, end = at + step * len;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int off = base + e * share;
+          int i = at <= off ? 0 : (at - off + stride - 1) / stride;  // the group's first end not before `at`
+          for (; i < C::kGroups && off + static_cast<long long>(i) * stride < end; ++i) {
+            const int in = off + i * stride - at, hh = in / len, skip = max(in - hh * len - C::kUnitCost, 0);
+            if (e == 1) {
+              plan->to[i] = before + hh * n + skip;
+            } else {
+              const int h = h0 + hh;
+              plan->from[i] = before + hh * n + skip;
+              plan->skip[i] = skip;
+              plan->unit[i] =
+                  BatchUnit{s * p.b.n_kv + h, h, seq.r0, seq.rows, seq.pos0, seq_first_tile(p, seq), n};
+            }
           }
-          if (has1 && w1 > at && w1 <= end) plan->end_tile = before + max(w1 - first, 0ll);
-          at = end;
-          before += n;
         }
+        at = end;
+        before += step * n;
       }
     }
     __syncthreads();
   }
-  const int n_tiles = static_cast<int>(plan->end_tile - plan->first_tile);
-  if (n_tiles == 0) return;  // nothing but the cost of a unit
+  const int n_tiles = plan->to[grp] - plan->from[grp];
+  if (n_tiles <= 0) return;
 
-  // ---- the group's ring.  Tiles are numbered along the CTA's stretch; group grp takes tiles k with
-  // k % kGroups == grp, its j-th being k = grp + j kGroups in stage j % kStages.  The producer is
-  // the group's first warp: lane 0 announces a tile, lane r copies region r.
-  uint64_t* gfull = full + grp * C::kStages;
-  uint64_t* gempty = empty + grp * C::kStages;
-  int* gkey = st_key + grp * C::kStages;
-  uint8_t* ring = smem + grp * C::kStages * C::kTileBytes;
+  // ---- the group's ring: its tile k goes to stage k % kStages.  Every warp of the group keeps the
+  // same account and copies its share of each tile (every NT-th 512 bytes).
+  const uint32_t ring = smem_u32(smem + grp * C::kStages * C::kTileBytes);
+  Producer* prod = &plan->producer[warp];
 
-  // region r of this lane, in units of 256 bytes: where it starts in a page, its bytes per tile, and
-  // where it goes in a stage
-  uint32_t region = 0;
-#pragma unroll
-  for (int r = 0; r < F::kKRegions; ++r)
-    if (lane == r) region = F::k_reg_off(r) / 256 | F::k_reg_tile(r) / 256 << 8 | L::k_off(r) / 256 << 16;
-#pragma unroll
-  for (int r = 0; r < F::kVRegions; ++r)
-    if (lane == F::kKRegions + r)
-      region = F::v_reg_off(r) / 256 | F::v_reg_tile(r) / 256 << 8 | (L::kKBytes + L::v_off(r)) / 256 << 16;
-
-  int p_page = -1, p_block = -1;  // page and logical block of the next tile to issue, loaded a tile ahead
   auto start_unit = [&](const BatchUnit& w, int start) {
-    if (lane == 0)
-      *prod = Producer{w.unit, start, w.t0, w.n, w.pos0 + w.rows - 1, p.window > 0 ? max(0, w.pos0 - p.window + 1) : 0};
+    if (lane == 0) {
+      prod->unit = w.unit;
+      prod->start = start;
+      prod->t0 = w.t0;
+      prod->n = w.n;
+      prod->last = w.pos0 + w.rows - 1;
+      prod->low = p.window > 0 ? max(0, w.pos0 - p.window + 1) : 0;
+    }
     __syncwarp();
   };
-  // page and logical block of tile k of the producer's unit
-  auto page_of = [&](int k) -> int2 {
-    const int u = lds_int(&prod->unit);
-    const int i = (lds_int(&prod->t0) + k - lds_int(&prod->start)) >> 3;
+  // entry i of unit u's list: page (-2: none there) and logical block
+  auto page_of = [&](int u, int i) -> int2 {
     const long long at = static_cast<long long>(u) * p.b.max_blocks + i;
     const bool any = i < p.b.max_blocks && (!p.n_list || i < p.n_list[u]);
     return make_int2(any ? p.b.page_table[at] : -2, any && p.page_logical ? p.page_logical[at] : i);
   };
-  // looks up the page of the group's tile jj (the issue that follows uses it, a tile's arithmetic later)
-  auto look_up = [&](int jj) {
-    const int k = grp + jj * C::kGroups;
-    if (k >= n_tiles) return;
-    while (true) {
-      const int end = lds_int(&prod->start) + lds_int(&prod->n);
-      if (k < end) break;
-      const int u = lds_int(&prod->unit);
-      __syncwarp();
-      start_unit(next_unit(p, u), end);
-    }
-    const int2 at = page_of(k);
-    p_page = at.x;
-    p_block = at.y;
-  };
-  // copies the group's tile jj into its stage
-  auto issue = [&](int jj) {
-    const int k = grp + jj * C::kGroups;
-    if (k >= n_tiles) return;
-    const int st = jj % C::kStages;
-    const int G = (lds_int(&prod->t0) + k - lds_int(&prod->start)) & 7;
-    const int last = lds_int(&prod->last);
-    // a tile that no row sees is not fetched
-    bool fetch = p_page != -2 && p_block >= 0 && p_block <= last / kPageTokens;
-    const int key = fetch ? p_block * kPageTokens + 16 * G : -1;
-    fetch = fetch && key <= last && key + 15 >= lds_int(&prod->low);
-    if (fetch && (p_page < 0 || p_page >= p.b.n_pages)) {
+  // Makes entry `e` the page at hand.  A block that no row sees has nothing to fetch, whatever its id.
+  auto open_page = [&](int2 e) {
+    const int last = lds_int(&prod->last), low = lds_int(&prod->low);
+    bool fetch = e.x != -2 && e.y >= 0 && e.y <= last / kPageTokens && e.y >= low / kPageTokens;
+    if (fetch && (e.x < 0 || e.x >= p.b.n_pages)) {
       if (lane == 0) record_error(KVATTN_ERR_BAD_PAGE);
       fetch = false;
     }
     if (lane == 0) {
-      *reinterpret_cast<volatile int*>(&gkey[st]) = fetch ? key : -1;
-      if (fetch)
-        mbar_arrive_expect_tx(&gfull[st], C::kTileBytes);
-      else
-        mbar_arrive(&gfull[st]);
+      prod->key0 = fetch ? e.y * kPageTokens : -1;
+      prod->k = p.b.k_pool + e.x * p.b.k_stride;  // used only when fetched
+      prod->v = p.b.v_pool + e.x * p.b.v_stride;
     }
     __syncwarp();
-    if (fetch && lane < C::kRegions) {
-      const uint32_t bytes = (region & 0xFF00u);
-      const uint8_t* pool = lane >= F::kKRegions ? p.b.v_pool + p_page * p.b.v_stride : p.b.k_pool + p_page * p.b.k_stride;
-      bulk_g2s(ring + st * C::kTileBytes + (region >> 16) * 256, pool + (region & 0xFFu) * 256 + G * bytes, bytes,
-               &gfull[st]);
-    }
   };
-  int j = 0;  // tiles this group has consumed
-  int start = plan->start;
-  const uint32_t q_s = smem_u32(smem + C::kSharedOff);
-  bool ok = true;
-  if (nt0 == 0) start_unit(plan->unit, start);
+  int2 ahead = make_int2(-2, 0);  // the entry after the page at hand, loaded when that was opened
+  // starts the copies of tile k; one group of copies per call, an empty one past the end
+  auto issue = [&](int k) {
+    if (k < n_tiles) {
+      int u = lds_int(&prod->unit), start = lds_int(&prod->start);
+      int end = start + lds_int(&prod->n);
+      int j = lds_int(&prod->t0) + k - start;  // the tile in the unit's list
+      if (k >= end) {
+        __syncwarp();
+        const BatchUnit w = next_unit(p, u);
+        start_unit(w, end);
+        u = w.unit;
+        start = end;
+        end += w.n;
+        j = w.t0;
+        ahead = page_of(u, j >> 3);
+      }
+      const int G = j & 7;
+      if (k > 0 && (G == 0 || k == start)) {
+        open_page(ahead);
+        if (k + 8 - G < end) ahead = page_of(u, (j >> 3) + 1);
+      }
+      const int key0 = lds_int(&prod->key0), key = key0 + 16 * G, st = k % C::kStages;
+      const bool fetch = key0 >= 0 && key <= lds_int(&prod->last) && key + 15 >= lds_int(&prod->low);
+      if (lane == 0) *reinterpret_cast<volatile int*>(&key_of[st]) = fetch ? key : -1;
+      if (fetch) {
+        const uint8_t* k_page = lds_ptr(&prod->k) + 16 * lane;
+        const uint8_t* v_page = lds_ptr(&prod->v) + 16 * lane;
+        const uint32_t to = ring + st * C::kTileBytes + 16 * lane;
+        int turn = 0;  // constant in the unrolled code
+        auto mine = [&]() { return NT == 1 || turn++ % NT == nt0; };
+        const uint8_t* src = k_page + G * L::kKCodes;
+#pragma unroll
+        for (int i = 0; i < L::kKCodes; i += 512)
+          if (mine()) cp16(to + i, src + i);
+        if constexpr (F::kK5) {
+          if (mine()) cp16(to + L::kKHigh, k_page + kK5HighOffset + G * 512);
+        }
+        src = v_page + G * L::kVCodes;
+#pragma unroll
+        for (int i = 0; i < L::kVCodes; i += 512)
+          if (mine()) cp16(to + L::kV + i, src + i);
+        // 256 bytes each: lanes 0-15 the K scales, 16-31 the V scales, then 0-15 the minima
+        const uint8_t* narrow = lane < 16 ? k_page + F::kKScaleOff : v_page + (F::kVScaleOff - 256);
+        if (mine()) cp16(to + L::kSmall, narrow + G * 256);
+        if constexpr (F::kKMin || F::kVMin) {
+          const uint8_t* low = F::kKMin ? k_page + kK5MinOffset : v_page + kV41MinOffset;
+          if (mine() && lane < 16) cp16(to + L::kSmall + 512, low + G * 256);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 
-  for (int done = 0; done < n_tiles;) {
-    const BatchUnit un = plan->unit;
-    const int end = min(start + un.n, n_tiles);  // this CTA's tiles of the unit: [done, end)
+  BatchUnit* mine = &plan->at_work[warp];
+  int start = -plan->skip[grp];  // first tile of the unit, in the group's numbering
+  int k = 0;                     // tiles this group has consumed
+  const uint32_t q_s = smem_u32(smem + C::kQOff + warp * C::kQWarpBytes);  // each warp its own fragments
+  if (lane == 0) *mine = plan->unit[grp];
+  __syncwarp();
+  start_unit(*mine, start);
+
+  while (true) {
+    const BatchUnit un = *mine;
+    const int end = min(start + un.n, n_tiles);  // the group's tiles of the unit: [k, end)
 
     // ---- the query's fragments.  A row is scaled by the power of two that puts its largest
     // magnitude into [1, 2) (exact), and split into f16 parts.
     float crow[2];
     uint32_t qsb_hi = 0u, qsb_lo = 0u;
     {
-      // every load before any use: the pages of the ring's first tiles (lane jj the group's tile
-      // jj), then the query rows
-      int2 ahead = make_int2(-2, 0);
-      const int k_ahead = grp + lane * C::kGroups;
-      if (done == 0 && nt0 == 0 && lane < C::kStages && k_ahead < end) ahead = page_of(k_ahead);
+      // every load before any use: the first two pages, then the query rows
+      int2 here = make_int2(-2, 0);
+      if (k == 0) {
+        const int i = (un.t0 - start) >> 3;
+        here = page_of(un.unit, i);
+        ahead = page_of(un.unit, i + 1);
+      }
       const int r = nt0 * 8 + g;
       Raw8<T> raw[kBlocks];
       const bool live = r < un.rows * p.group;
@@ -362,14 +399,9 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) raw[b] = load_raw8<T>(p.q.data, at + 32 * b + 8 * t);
       }
-      if (done == 0 && nt0 == 0) {
-        for (int jj = 0; jj < C::kStages; ++jj) {
-          p_page = __shfl_sync(0xffffffffu, ahead.x, jj);
-          p_block = __shfl_sync(0xffffffffu, ahead.y, jj);
-          if (grp + jj * C::kGroups >= end) look_up(jj);  // already another unit's
-          issue(jj);
-        }
-        look_up(C::kStages);
+      if (k == 0) {
+        open_page(here);
+        for (int i = 0; i < C::kStages - (NT > 1); ++i) issue(i);
       }
       float x[kBlocks][8];
 #pragma unroll
@@ -397,20 +429,18 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
         float xv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) xv[e] = x[bl][e] * inv;
-        if (bl % C::kGroups == grp) {  // the groups hold the same rows: each writes its share
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            uint32_t hi[2], lo[2];
-            split_pair(xv[4 * ks], xv[4 * ks + 1], hi[0], lo[0]);
-            split_pair(xv[4 * ks + 2], xv[4 * ks + 3], hi[1], lo[1]);
-            const uint32_t to = q_s + (((bl * 2 + ks) * NT + nt0) * 32 + lane) * C::kQFragBytes;
-            if constexpr (QP == 2)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(lo[0]),
-                           "r"(lo[1])
-                           : "memory");
-            else
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(hi[0]), "r"(hi[1]) : "memory");
-          }
+        for (int ks = 0; ks < 2; ++ks) {
+          uint32_t hi[2], lo[2];
+          split_pair(xv[4 * ks], xv[4 * ks + 1], hi[0], lo[0]);
+          split_pair(xv[4 * ks + 2], xv[4 * ks + 3], hi[1], lo[1]);
+          const uint32_t to = q_s + ((bl * 2 + ks) * 32 + lane) * C::kQFragBytes;
+          if constexpr (QP == 2)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(lo[0]),
+                         "r"(lo[1])
+                         : "memory");
+          else
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(hi[0]), "r"(hi[1]) : "memory");
         }
         if constexpr (F::kKMin) {
           float sm = 0.f;
@@ -427,9 +457,10 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
       crow[0] = __shfl_sync(0xffffffffu, cr, (2 * t) * 4);
       crow[1] = __shfl_sync(0xffffffffu, cr, (2 * t + 1) * 4);
     }
-    __syncthreads();
+    __syncwarp();
+    // a fragment is read by the lane that wrote it
     auto qfrag = [&](int bl, int ks) -> uint4 {
-      const uint32_t from = q_s + (((bl * 2 + ks) * NT + nt0) * 32 + lane) * C::kQFragBytes;
+      const uint32_t from = q_s + ((bl * 2 + ks) * 32 + lane) * C::kQFragBytes;
       if constexpr (QP == 2) {
         return lds128(from);
       } else {
@@ -439,10 +470,9 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
       }
     };
 
-    // ---- this group's tiles of the unit
+    // ---- the tiles
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     float oacc[2 * kTileBlocks][4], racc[4] = {0.f, 0.f, 0.f, 0.f};
-    BatchUnit next{};  // the last warp's lane 0: the unit after this one
 #pragma unroll
     for (int i = 0; i < 2 * kTileBlocks; ++i)
 #pragma unroll
@@ -453,57 +483,40 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
     for (int c = 0; c < 2; ++c) qpos[c] = un.pos0 + min((nt0 * 8 + 2 * t + c) / p.group, un.rows - 1);
     const int last = un.pos0 + un.rows - 1;
     const int span = p.window > 0 ? p.window : INT_MAX;
-    for (; grp + j * C::kGroups < end; ++j) {
-      const int st = j % C::kStages;
-      const uint32_t par = (j / C::kStages) & 1;
-      if (!mbar_wait(&gfull[st], par)) {
-        ok = false;
-        break;
+    for (; k < end; ++k) {
+      const int st = k % C::kStages;
+      // this warp's copies of tile k are done, and with the barrier everybody's are seen
+      if constexpr (NT == 1) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+        __syncwarp();
+      } else {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+        asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "n"(NT * 32) : "memory");
+        issue(k + C::kStages - 1);  // into the stage of tile k - 1, which the group is done with
       }
-      const int key = *reinterpret_cast<volatile int*>(&gkey[st]);
+      const int key = *reinterpret_cast<volatile int*>(&key_of[st]);
       if (key >= 0) {
-        uint8_t* tile = ring + st * C::kTileBytes;
-        if (key + 15 > last)
-          blank_tokens(tile + L::kKBytes + L::kVScale, F::kVMin ? tile + L::kKBytes + L::kVMinimum : nullptr, lane,
-                       last - key + 1);
+        const uint32_t kb = ring + st * C::kTileBytes;
+        if (key + 15 > last) {
+          uint8_t* vs = smem + (kb - smem_u32(smem)) + L::kV + L::kVScale;
+          blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
+        }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
-        const uint32_t kb = smem_u32(tile);
         attend_tile<L, KF, VF, QP, PP>(
-            kb, kb + L::kKBytes, 0, g, t, qfrag, qsb_hi, qsb_lo, crow, 2.f,
+            kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow, 2.f,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
               return need_mask && (at > qpos[e & 1] || at <= qpos[e & 1] - span) ? -INFINITY : x;
             },
             m_run, l_run, oacc, racc);
       }
-      __syncwarp();
       if constexpr (NT == 1) {
-        issue(j + C::kStages);
-        look_up(j + C::kStages + 1);
-      } else {
-        // the producer refills the stage of the tile before this one: the other warps are done
-        // with it, or nearly
-        if (lane == 0) mbar_arrive(&gempty[st]);
-        if (nt0 == 0 && j > 0) {
-          if (!mbar_wait(&gempty[(j - 1) % C::kStages], ((j - 1) / C::kStages) & 1)) {
-            ok = false;
-            break;
-          }
-          issue(j - 1 + C::kStages);
-          look_up(j + C::kStages);
-        }
+        __syncwarp();
+        issue(k + C::kStages);
       }
     }
 
-    // ---- merge the groups' states, pairwise through shared memory
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float l = l_run[c];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      l_run[c] = l;
-    }
+    // ---- the rows: 2t, 2t + 1 of the n-tile, dims 16 i + g, + 8
     if constexpr (F::kVMin) {
       // zero-point values: the minimum terms of block b for rows 2t, 2t + 1 sit in lane 4b + t
 #pragma unroll
@@ -518,122 +531,61 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, BatchCfg<KF
           }
         }
     }
-    if (!ok) *reinterpret_cast<volatile int*>(&plan->abort) = 1;
-    float4* slots = reinterpret_cast<float4*>(smem + C::kSharedOff);
-    constexpr int kSlot4 = C::kSlotBytes / 16;  // float4s of a slot; (m, l) behind the 16 x 32 of o
+    BatchUnit w;  // the unit again
+    w.unit = lds_int(&mine->unit);
+    w.h = lds_int(&mine->h);
+    w.r0 = lds_int(&mine->r0);
+    w.n = lds_int(&mine->n);
+    const int n_rows = lds_int(&mine->rows) * p.group;
+    const bool whole = start >= 0 && start + w.n <= n_tiles;
+    const int slot = (grp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)) * 2 + (start <= 0 ? 0 : 1);
 #pragma unroll
-    for (int half = C::kGroups / 2; half >= 1; half /= 2) {
-      __syncthreads();  // the query fragments, or the slots of the round before, are done with
-      if (grp >= half && grp < 2 * half) {
-        float4* to = slots + ((grp - half) * NT + nt0) * kSlot4 + lane;
-#pragma unroll
-        for (int i = 0; i < 2 * kTileBlocks; ++i) to[32 * i] = make_float4(oacc[i][0], oacc[i][1], oacc[i][2], oacc[i][3]);
-        to[32 * 2 * kTileBlocks] = make_float4(m_run[0], m_run[1], l_run[0], l_run[1]);
-        // the last warp, now idle, looks up the next unit and fetches its query rows into L2
-        if (warp == C::kWarps - 1 && end < n_tiles) {
-          const BatchUnit nx = next_unit(p, un.unit);
-          if (lane < nx.rows * p.group) {
-            const int qi = lane / p.group;
-            const char* row = static_cast<const char*>(p.q.data) +
-                              sizeof(T) * ((nx.r0 + qi) * p.q.row_stride +
-                                           (nx.h * p.group + lane - qi * p.group) * p.q.head_stride);
-#pragma unroll
-            for (int b = 0; b < kHeadDim * static_cast<int>(sizeof(T)); b += 128)
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(row + b));
-          }
-          if (lane == 0) next = nx;
-        }
-      }
-      __syncthreads();
-      if (grp < half) {
-        const float4* from = slots + (grp * NT + nt0) * kSlot4 + lane;
-        const float4 ml = from[32 * 2 * kTileBlocks];
-        const float om[2] = {ml.x, ml.y}, ol[2] = {ml.z, ml.w};
-        float wa[2], wb[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          // a state that saw no key has m = -inf, l = 0 and o = 0: its weight is 0 (and a NaN in l or o stays one)
-          const float M = fmaxf(m_run[c], om[c]), mu = M == -INFINITY ? 0.f : M;
-          wa[c] = fast_exp2(m_run[c] - mu);
-          wb[c] = fast_exp2(om[c] - mu);
-          l_run[c] = l_run[c] * wa[c] + ol[c] * wb[c];
-          m_run[c] = M;
-        }
+    for (int c = 0; c < 2; ++c) {
+      float l = l_run[c];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      // a row that saw no key: l = 0 (a NaN stays one)
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m_run[c] + log2f(l);
+      const int row = nt0 * 8 + 2 * t + c;
+      if (row >= n_rows) continue;
+      if (whole) {
+        const int qi = row / p.group, hq = w.h * p.group + row - qi * p.group;
+        T* to = static_cast<T*>(p.out.data) + (w.r0 + qi) * p.out.row_stride + hq * p.out.head_stride + g;
 #pragma unroll
         for (int i = 0; i < 2 * kTileBlocks; ++i) {
-          const float4 o = from[32 * i];
-          oacc[i][0] = oacc[i][0] * wa[0] + o.x * wb[0];
-          oacc[i][1] = oacc[i][1] * wa[1] + o.y * wb[1];
-          oacc[i][2] = oacc[i][2] * wa[0] + o.z * wb[0];
-          oacc[i][3] = oacc[i][3] * wa[1] + o.w * wb[1];
+          to[16 * i] = static_cast<T>(oacc[i][c] * inv);
+          to[16 * i + 8] = static_cast<T>(oacc[i][c + 2] * inv);
         }
-      }
-    }
-    __syncthreads();
-    if (plan->abort) break;
-    if (grp == 0) {
-      // rows of 256 through the warp's slot, so that lanes store whole lines
-      float* rows = reinterpret_cast<float*>(slots + nt0 * kSlot4);
-      float lse2[2];
+        if (g == 0)
+          p.lse[static_cast<long long>(w.r0 + qi) * (p.b.n_kv * p.group) + hq] = lse2 * 0.69314718055994531f;
+      } else {
+        const long long at = static_cast<long long>(slot) * C::kRowsPad + row;
+        float* to = p.part_o + at * kHeadDim + g;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float inv = l_run[c] == 0.f ? 0.f : 1.f / l_run[c];
-        lse2[c] = l_run[c] == 0.f ? -INFINITY : m_run[c] + log2f(l_run[c]);
-#pragma unroll
-        for (int i = 0; i < 2 * kTileBlocks; ++i)
-#pragma unroll
-          for (int hi = 0; hi < 2; ++hi)
-            rows[(2 * t + c) * C::kOStride + 16 * i + g + 8 * hi] = oacc[i][c + 2 * hi] * inv;
-      }
-      __syncwarp();
-      const int r0 = lds_int(&plan->unit.r0), n_rows = lds_int(&plan->unit.rows) * p.group;
-      const int h = lds_int(&plan->unit.h), unit_n = lds_int(&plan->unit.n);
-      const bool whole = start >= 0 && start + unit_n <= n_tiles;
-      const int slot = static_cast<int>(blockIdx.x) * 2 + (start <= 0 ? 0 : 1);
-      const long long part = static_cast<long long>(slot) * C::kRowsPad;
-#pragma unroll 1
-      for (int r = 0; r < 8; ++r) {
-        const int row = nt0 * 8 + r;
-        if (row >= n_rows) break;
-        const float* from = rows + r * C::kOStride + 8 * lane;
-        const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
-        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const float l2 = __shfl_sync(0xffffffffu, r & 1 ? lse2[1] : lse2[0], r >> 1);
-        if (whole) {
-          const int qi = row / p.group, hq = h * p.group + row - qi * p.group;
-          store8<T>(p.out.data, (r0 + qi) * p.out.row_stride + hq * p.out.head_stride + 8 * lane, x);
-          if (lane == 0)
-            p.lse[static_cast<long long>(r0 + qi) * (p.b.n_kv * p.group) + hq] = l2 * 0.69314718055994531f;
-        } else {
-          store8<float>(p.part_o, (part + row) * kHeadDim + 8 * lane, x);
-          if (lane == 0) p.part_lse[part + row] = l2;
+        for (int i = 0; i < 2 * kTileBlocks; ++i) {
+          to[16 * i] = oacc[i][c] * inv;
+          to[16 * i + 8] = oacc[i][c + 2] * inv;
         }
-      }
-      if (threadIdx.x == 0) {
-        int2* parts = p.unit_parts + lds_int(&plan->unit.unit);
-        if (start >= 0) parts->x = slot;
-        if (start + unit_n <= n_tiles) parts->y = static_cast<int>(blockIdx.x);
+        if (g == 0) p.part_lse[at] = lse2;
       }
     }
-    done = end;
-    start = end;
-    __syncthreads();  // the slots and the plan's unit, before the next unit's
-    if (done < n_tiles) {
-      if (warp == C::kWarps - 1 && lane == 0) plan->unit = next;
-      __syncthreads();
+    if (nt0 == 0 && lane == 0) {
+      int2* parts = p.unit_parts + w.unit;
+      if (start >= 0) parts->x = slot;
+      if (start + w.n <= n_tiles) parts->y = slot >> 1;
     }
-  }
-  if (plan->abort && nt0 == 0 && lane == 0) {
-    // a bounded wait expired: wait (bounded) for the copies still in flight, then leave
-    const int issued = min(j + C::kStages, (n_tiles - grp + C::kGroups - 1) / C::kGroups);
-    const unsigned long long t0 = global_timer_ns();
-    for (int jj = max(0, issued - C::kStages); jj < issued; ++jj)
-      while (!mbar_try_wait(&gfull[jj % C::kStages], (jj / C::kStages) & 1))
-        if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+    if (k == n_tiles) break;
+    start = k;
+    const BatchUnit nx = next_unit(p, w.unit);
+    __syncwarp();  // every lane has read the unit and its fragments
+    if (lane == 0) *mine = nx;
+    __syncwarp();
   }
 }
 
-// Merges the partials of the units that more than one CTA took part in.  One CTA per unit (and
+// Merges the partials of the units that more than one group took part in.  One CTA per unit (and
 // per row, where there are few units), 256 threads = four groups of 64 (four channels each); a
 // group takes every fourth part, loading a batch of them before using any, and the groups are
 // combined once through shared memory.
@@ -651,7 +603,7 @@ __global__ void __launch_bounds__(256) merge_batch_kernel(const BatchDecodeParam
   if (un.n == 0) return;
   const int2 parts = p.unit_parts[u];
   const int c0 = parts.x >> 1, n_parts = parts.y - c0 + 1;
-  if (n_parts == 1) return;  // written by its CTA
+  if (n_parts == 1) return;  // written by its group
   const int tid = threadIdx.x, grp = tid >> 6, d4 = tid & 63;
   for (int row = blockIdx.y; row < un.rows * p.group; row += gridDim.y) {
     float m = -INFINITY, l = 0.f;
@@ -720,8 +672,8 @@ __global__ void __launch_bounds__(256) merge_batch_kernel(const BatchDecodeParam
 // ---------------------------------------------------------------------------------------
 int batch_row_tiles(int rows) { return (rows + 7) / 8; }
 
-// CTAs that the split grid can have: the workspace is sized by it.
-int batch_grid_bound(int sms, int n_tiles8) { return sms * (n_tiles8 < 3 ? 3 : 2); }
+// Groups that the split grid can have: the workspace is sized by it.
+int batch_group_bound(int sms, int n_tiles8) { return sms * (12 / n_tiles8); }
 
 template <int KF, int VF, int NT, typename T>
 static cudaError_t launch_batch_t(const BatchDecodeParams& p, int sms, long long most_tiles, cudaStream_t stream) {
@@ -731,8 +683,8 @@ static cudaError_t launch_batch_t(const BatchDecodeParams& p, int sms, long long
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(
-      std::min(static_cast<long long>(sms) * C::kCtas, (most_tiles + C::kUnitCost * units) / C::kMinShare + 1)));
+  const long long groups = (most_tiles + C::kUnitCost * units) / C::kMinShare + 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(sms, (groups + C::kGroups - 1) / C::kGroups)));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;

@@ -85,15 +85,19 @@ struct PageLayout {
   static constexpr int kVScale = F::kVScaleOff, kVMinimum = kV41MinOffset;
 };
 
-// ... or one tile by itself, its part of every region packed behind the one before (G = 0).
+// ... or one tile by itself (G = 0), its part of every region packed: the wide ones first (K codes,
+// fifth bits, V codes; multiples of 512 bytes), then the 256-byte ones (scales, minima).  Offsets of
+// the V parts are from the V codes, as in a page.
 template <int KF, int VF>
 struct SingleTileLayout {
   using F = TileFormat<KF, VF>;
-  __host__ __device__ static constexpr int k_off(int r) { return r == 0 ? 0 : k_off(r - 1) + F::k_reg_tile(r - 1); }
-  __host__ __device__ static constexpr int v_off(int r) { return r == 0 ? 0 : v_off(r - 1) + F::v_reg_tile(r - 1); }
-  static constexpr int kKHigh = k_off(1), kKScale = F::kK5 ? k_off(2) : k_off(1), kKMinimum = k_off(3);
-  static constexpr int kVScale = v_off(1), kVMinimum = v_off(2);
-  static constexpr int kKBytes = k_off(F::kKRegions), kVBytes = v_off(F::kVRegions);
+  static constexpr int kKCodes = F::k_reg_tile(0), kHigh = F::kK5 ? F::k_reg_tile(1) : 0, kVCodes = F::v_reg_tile(0);
+  static constexpr int kKHigh = kKCodes, kV = kKCodes + kHigh;  // from the tile's start
+  static constexpr int kSmall = kV + kVCodes, kNarrow = 2 + F::kKMin + F::kVMin;
+  static constexpr int kKScale = kSmall, kKMinimum = kSmall + 512;
+  static constexpr int kVScale = kSmall + 256 - kV, kVMinimum = kSmall + 512 - kV;
+  static_assert(!(F::kKMin && F::kVMin), "one minimum: the third 256 bytes");
+  static constexpr int kBytes = kSmall + 256 * kNarrow;
 };
 
 // Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
