@@ -447,8 +447,9 @@ typedef struct kvattn_rows {
  * batch) are neither read nor written.
  * Checked on the device, because the arrays live there: 0 <= row_start[s] <= row_start[s + 1]
  * <= n_rows, at most max_rows rows, pos_start[s] >= 0 and the last position inside max_blocks
- * blocks.  A sequence that breaks one of these is left out (none of its rows is written) and
- * KVATTN_ERR_INVALID_ARG is recorded in the device error word. */
+ * blocks.  A sequence that breaks one of these is left out (none of its rows is written), and
+ * where row_start does not ascend others may be too; KVATTN_ERR_INVALID_ARG is recorded in the
+ * device error word. */
 typedef struct kvattn_batch {
   const int32_t* row_start;  /* device int32 [n_seqs + 1], ascending                        */
   const int32_t* pos_start;  /* device int32 [n_seqs]                                       */

@@ -117,21 +117,4 @@ __device__ __forceinline__ BatchSeq load_seq(const BatchParams& p, int s, bool c
   return q;
 }
 
-// The last sequence whose first row is <= row, by the whole warp (32 candidates a step): the
-// one that holds the row, unless the row lies in the padding (the caller checks).  -1: before
-// the first sequence.  Any contents of row_start keep the answer inside [-1, n_seqs).
-__device__ __forceinline__ int find_seq(const int32_t* row_start, int n_seqs, int row, int lane) {
-  int lo = 0, hi = n_seqs;
-  while (true) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + lane * step;
-    const bool le = at < hi && row_start[at] <= row;
-    const int n = __popc(__ballot_sync(0xffffffffu, le));
-    if (n == 0) return lo == 0 ? -1 : lo;
-    lo += (n - 1) * step;
-    hi = min(hi, lo + step);
-    if (step == 1) return lo;
-  }
-}
-
 }  // namespace kvattn

@@ -83,6 +83,11 @@ BatchPlan plan_batch(const kvattn_kv_desc* d, const kvattn_batch* b) {
   return p;
 }
 
+// The grid of append and read: four warps per (tile slot, head), two such per CTA.
+bool too_many_tiles(const kvattn_kv_desc* d, const kvattn_batch* b) {
+  return (b->n_rows / 16 + 2ll * b->n_seqs) * d->n_kv_heads / 2 >= INT32_MAX;
+}
+
 bool nothing_to_do(const kvattn_batch* b) { return b->n_seqs == 0 || b->n_rows == 0 || b->max_rows == 0; }
 
 }  // namespace
@@ -98,7 +103,7 @@ KVATTN_API int kvattn_append_batch(const kvattn_kv_desc* desc, const kvattn_batc
   if ((st = validate_rows(k, batch->n_rows, desc->n_kv_heads, false))) return st;
   if ((st = validate_rows(v, batch->n_rows, desc->n_kv_heads, false))) return st;
   if (k->dtype != v->dtype) return KVATTN_ERR_UNSUPPORTED_FORMAT;
-  if (batch->n_rows * desc->n_kv_heads > INT32_MAX) return KVATTN_ERR_UNSUPPORTED_SHAPE;
+  if (too_many_tiles(desc, batch)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
   int dev;
   if ((st = current_device_checked(&dev))) return st;
   const cudaError_t e = launch_append_batch(params_of(desc, batch), view_of(k, batch->n_rows, desc->n_kv_heads),
@@ -117,7 +122,7 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
   if (k && (st = validate_rows(k, batch->n_rows, desc->n_kv_heads, true))) return st;
   if (v && (st = validate_rows(v, batch->n_rows, desc->n_kv_heads, true))) return st;
   if (k && v && k->dtype != v->dtype) return KVATTN_ERR_UNSUPPORTED_FORMAT;
-  if (batch->n_rows * desc->n_kv_heads > INT32_MAX) return KVATTN_ERR_UNSUPPORTED_SHAPE;
+  if (too_many_tiles(desc, batch)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
   int dev;
   if ((st = current_device_checked(&dev))) return st;
   const RowsView none{nullptr, 0, 0};

@@ -1,88 +1,231 @@
 // The cache of a ragged batch, written and read back (kvattn_append_batch, kvattn_read_batch).
 //
-// One warp takes one (row, KV head): lane l owns channels [8l, 8l + 8), four lanes form one
-// 32-channel block, as in the single-sequence encoder.
+// One warp takes a quarter (64 channels of K and of V) of one (tile of 16 positions of a sequence, KV
+// head): a whole tile a warp left a prompt of a few thousand tokens with too few warps (49.8 us for
+// six prompts against TWO).  A page's codes and scales sit
+// in tensor-core fragment order by such tiles, so a tile is a few contiguous ranges of the page, and
+// lane (g, t) = (lane / 4, lane % 4) of a warp that holds rows 8H + g, channels 32b + 8t .. + 7 of
+// every block b holds, block by block, exactly the keys' bytes it stores: 16 of them per 64
+// channels.  The four lanes of a quad form one 32-channel block, as in the single-sequence encoder.
+// Values are stored transposed (a lane's bytes belong to four tokens), which takes four shuffles
+// per block and eight tokens.  Both directions are bound by HBM: a bf16 tile is 16,384 bytes of rows
+// and 6,656 (Q8_0 / Q4_0) of page.
+//
+// A tile that the call's rows fill in part is written token by token with byte stores (its other
+// tokens' bits share bytes and words with them, and stay).
 #include "batch.cuh"
 #include "decode.cuh"
 
 namespace kvattn {
 
-// The value that slot `tok` of a key page holds for channels 8 lane .. 8 lane + 7: the reader's
-// side of encode_token.
-__device__ __forceinline__ void decode_key8(const uint8_t* pg, int tok, int lane, int fmt, float (&x)[8]) {
-  const int G = tok >> 4, H = (tok >> 3) & 1, R = tok & 7;
-  const int b = lane >> 2, T = lane & 3;
-  const int si = 2 * (((G * 8 + R) * 2 + H) * 8 + b);
-  if (fmt == kKeyQ8) {
-    const uint2 w = *reinterpret_cast<const uint2*>(
-        pg + ((((G * 4 + (lane >> 3)) * 2 + H) * 8 + R) * 4 + T) * 16 + 8 * ((lane & 7) >> 2));
-    const float d = __half2float(*reinterpret_cast<const __half*>(pg + kKScaleOffset + si));
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      x[e] = (static_cast<int>(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 255u) - 128) * d;
-    return;
-  }
-  const int c = b & 3, line = (((G * 2 + (b >> 2)) * 2 + H) * 8 + R) * 4 + T;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(pg + 4 * (line * 4 + c));
-  uint32_t hb = 0;
-  float d, m = 0.f;
-  int off = 0;
-  if (fmt == kKeyQ4) {
-    d = __half2float(*reinterpret_cast<const __half*>(pg + kK4ScaleOffset + si));
-    off = 8;
-  } else {
-    hb = *reinterpret_cast<const uint32_t*>(pg + kK5HighOffset + 4 * line);
-    d = __half2float(*reinterpret_cast<const __half*>(pg + kK5ScaleOffset + si));
-    if (fmt == kKeyQ51)
-      m = __half2float(*reinterpret_cast<const __half*>(pg + kK5MinOffset + si));
-    else
-      off = 16;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t lo = (w >> (4 * (e >> 1) + 16 * (e & 1))) & 15u;
-    const uint32_t hi = (hb >> (16 * (e & 1) + 4 * c + (e >> 1))) & 1u;
-    x[e] = fmaf(static_cast<float>(static_cast<int>(lo | (hi << 4)) - off), d, m);
-  }
+// One warp's share: KV head h, tile `tile` (of the sequence's 16-token tiles) of sequence s, its
+// rows [r0, r0 + n) at slots [slot, slot + n) of page `page` (-1: a bad id).
+struct TileRows {
+  int s, page, slot, n;
+  long long r0;
+};
+
+// Tile slots: sequence s owns slots row_start[s] / 16 + 2 s ..., at least as many as its rows touch
+// tiles, so a slot's sequence is found by a search without any prefix sum.
+__device__ __forceinline__ long long slot_base(const int32_t* row_start, int s) {
+  return (static_cast<long long>(row_start[s]) >> 4) + 2ll * s;
 }
 
-__device__ __forceinline__ void decode_val8(const uint8_t* pg, int tok, int lane, int fmt, float (&x)[8]) {
-  const int G = tok >> 4, tl = tok & 15;
-  const int T = (tl & 7) >> 1, wlo = tl >> 3, ylo = tl & 1;
-  const int b = lane >> 2, cl = lane & 3;
-  const int si = 2 * (((G * 4 + T) * 8 + b) * 4 + ylo + 2 * wlo);
-  if (fmt == kValQ8) {
-    const float d = __half2float(*reinterpret_cast<const __half*>(pg + kV8ScaleOffset + si));
-    const uint8_t* at = pg + ((G * 8 + b) * 8 * 4 + T) * 16 + 4 * (2 * (cl >> 1) + wlo) + 2 * (cl & 1) + ylo;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (static_cast<int>(at[64 * e]) - 128) * d;
-    return;
+__device__ __forceinline__ bool locate_tile(const BatchParams& p, long long at, int h, int lane, TileRows* out) {
+  // the last sequence whose slots start at or before `at`, 32 candidates a step; whatever row_start
+  // holds, the answer stays inside [0, n_seqs) and is checked below
+  int lo = 0, hi = p.n_seqs;
+  while (true) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, i < hi && slot_base(p.row_start, i) <= at);
+    if (le == 0) return false;
+    lo += (31 - __clz(le)) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) break;
   }
-  const float d = __half2float(*reinterpret_cast<const __half*>(pg + kV4ScaleOffset + si));
-  const float m = fmt == kValQ41 ? __half2float(*reinterpret_cast<const __half*>(pg + kV41MinOffset + si)) : 0.f;
-  const int off = fmt == kValQ41 ? 0 : 8;
-  const uint8_t* at = pg + ((G * 4 + (b >> 1)) * 8 * 4 + T) * 16 + 4 * (2 * (b & 1) + wlo) + 2 * ylo + (cl >> 1);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    x[e] = fmaf(static_cast<float>(((at[64 * e] >> (4 * (cl & 1))) & 15) - off), d, m);
-}
-
-// The page and slot of row `row` for KV head h; false: the row belongs to no sequence, or to
-// one that a check left out.  page is -1 where the table's id is out of range.
-__device__ __forceinline__ bool locate_row(const BatchParams& p, int row, int h, int lane, int* page, int* slot) {
-  const int s = find_seq(p.row_start, p.n_seqs, row, lane);
-  if (s < 0) return false;
-  const BatchSeq q = load_seq(p, s, true);
-  if (row < q.r0 || row >= q.r0 + q.rows) return false;
-  const int pos = q.pos0 + (row - q.r0);
-  const int pg = p.page_table[(static_cast<long long>(s) * p.n_kv + h) * p.max_blocks + pos / kPageTokens];
-  *slot = pos % kPageTokens;
-  *page = pg;
-  if (pg < 0 || pg >= p.n_pages) {
-    record_error(KVATTN_ERR_BAD_PAGE);
-    *page = -1;
+  const BatchSeq q = load_seq(p, lo, true);
+  if (q.rows == 0) return false;
+  const long long tile = q.pos0 / 16 + (at - slot_base(p.row_start, lo));
+  const long long first = max(tile * 16, static_cast<long long>(q.pos0));
+  const long long end = min(tile * 16 + 16, static_cast<long long>(q.pos0) + q.rows);
+  if (tile < q.pos0 / 16 || first >= end) return false;
+  out->s = lo;
+  out->slot = static_cast<int>(first % kPageTokens);
+  out->n = static_cast<int>(end - first);
+  out->r0 = q.r0 + (first - q.pos0);
+  out->page = p.page_table[(static_cast<long long>(lo) * p.n_kv + h) * p.max_blocks + first / kPageTokens];
+  if (out->page < 0 || out->page >= p.n_pages) {
+    if (lane == 0) record_error(KVATTN_ERR_BAD_PAGE);
+    out->page = -1;
   }
   return true;
+}
+
+// ------------------------------------------------------------------------------ writing
+// Eight codes of a block (this lane's quarter) of either side's formats, with the scale and minimum
+// that every lane of the quad gets.  FMT: 8 (Q8_0, the byte q + 128), 4 / 50 (Q4_0 / Q5_0), 41 / 51.
+template <int FMT>
+__device__ __forceinline__ void encode8(const float (&x)[8], int lane, uint32_t (&q)[8], uint32_t* d16, uint32_t* m16) {
+  float inv, d, mn = 0.f;
+  if constexpr (FMT == KVATTN_FMT_Q8_0) {
+    d = q8_scale(x, &inv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = static_cast<uint32_t>(q8_code(x[e], inv) + 128);
+  } else if constexpr (FMT == KVATTN_FMT_Q4_0 || FMT == KVATTN_FMT_Q5_0) {
+    constexpr int kHalf = FMT == KVATTN_FMT_Q4_0 ? 8 : 16;
+    d = offset_scale<kHalf>(x, lane, &inv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = static_cast<uint32_t>(offset_code<kHalf>(x[e], inv));
+  } else {
+    constexpr int kTop = FMT == KVATTN_FMT_Q4_1 ? 15 : 31;
+    d = min_scale<kTop>(x, &mn, &inv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = static_cast<uint32_t>(min_code<kTop>(x[e], mn, inv));
+  }
+  *d16 = __half_as_ushort(__float2half_rn(d));
+  *m16 = __half_as_ushort(__float2half_rn(mn));
+}
+
+// Channels 64 P .. + 63 of a whole tile of keys: rows at `rows` (16 of them, row_stride apart), their
+// bytes to the page.
+template <typename T, int FMT>
+__device__ __forceinline__ void write_keys(const T* rows, long long row_stride, uint8_t* pg, int G, int P, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  constexpr bool k8 = FMT == KVATTN_FMT_Q8_0, k5 = FMT == KVATTN_FMT_Q5_0 || FMT == KVATTN_FMT_Q5_1;
+  constexpr int kScale = k8 ? kKScaleOffset : k5 ? kK5ScaleOffset : kK4ScaleOffset;
+  Raw8<T> raw[2][2];
+#pragma unroll
+  for (int H = 0; H < 2; ++H)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) raw[H][e] = load_raw8<T>(rows + (8 * H + g) * row_stride, 64 * P + 32 * e + 8 * t);
+#pragma unroll
+  for (int H = 0; H < 2; ++H) {
+    uint32_t q[2][8], d[2], m[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x[8];
+      widen8<T>(raw[H][e], x);
+      encode8<FMT>(x, lane, q[e], &d[e], &m[e]);
+    }
+    if constexpr (k8) {
+      // the lane's 16 bytes: block 2P in 0-7, block 2P + 1 in 8-15
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t* c = q[i >> 1] + 4 * (i & 1);
+        w[i] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+      }
+      *reinterpret_cast<uint4*>(pg + G * 4096 + ((((P * 2 + H) * 8 + g) * 4 + t) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      // two of the four words of the lane's 16 bytes; fifth bits: two of the four bytes of its word
+      const int line = ((((P >> 1) * 2 + H) * 8 + g) * 4 + t), c0 = 2 * (P & 1);
+      uint32_t w[2] = {0u, 0u}, high = 0;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          w[c] |= (q[c][e] & 15u) << (4 * (e >> 1) + 16 * (e & 1));
+          if constexpr (k5) high |= (q[c][e] >> 4) << (16 * (e & 1) + 4 * c + (e >> 1));
+        }
+      *reinterpret_cast<uint2*>(pg + G * 2048 + 16 * line + 4 * c0) = make_uint2(w[0], w[1]);
+      if constexpr (k5) {
+        uint8_t* to = pg + kK5HighOffset + G * 512 + 4 * line + (P & 1);
+        to[0] = static_cast<uint8_t>(high);
+        to[2] = static_cast<uint8_t>(high >> 16);
+      }
+    }
+    if (t == 0) {
+      const int si = G * 256 + ((g * 2 + H) * 8 + 2 * P) * 2;
+      *reinterpret_cast<uint32_t*>(pg + kScale + si) = d[0] | d[1] << 16;
+      if constexpr (FMT == KVATTN_FMT_Q5_1) *reinterpret_cast<uint32_t*>(pg + kK5MinOffset + si) = m[0] | m[1] << 16;
+    }
+  }
+}
+
+// Channels 64 C .. + 63 of a whole tile of values.  Lane (g, t) encodes token 8H + g, channels 32b + 8t
+// + e; lane (R, T) stores, per block, the codes of channels R, R + 8, R + 16, R + 24 of tokens 2T,
+// 2T + 1 (and + 8).
+template <typename T, int FMT>
+__device__ __forceinline__ void write_values(const T* rows, long long row_stride, uint8_t* pg, int G, int C, int lane) {
+  const int g = lane >> 2, t = lane & 3;  // as a source; as a target R = g, T = t
+  constexpr bool v8 = FMT == KVATTN_FMT_Q8_0;
+  constexpr int kScale = v8 ? kV8ScaleOffset : kV4ScaleOffset;
+  const int src = 8 * t + (g >> 2);  // lane (token 2T, channel group R / 4)
+  const uint32_t pick = g & 3;       // byte R % 4 of its word
+  Raw8<T> raw[2][2];
+#pragma unroll
+  for (int H = 0; H < 2; ++H)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) raw[H][e] = load_raw8<T>(rows + (8 * H + g) * row_stride, 64 * C + 32 * e + 8 * t);
+  uint32_t w[2][4];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int b = 2 * C + e;
+#pragma unroll
+    for (int H = 0; H < 2; ++H) {
+      float x[8];
+      uint32_t q[8], d, m;
+      widen8<T>(raw[H][e], x);
+      encode8<FMT>(x, lane, q, &d, &m);
+      if (t == 0) {
+        const int si = G * 256 + (((g >> 1) * 8 + b) * 4 + (g & 1) + 2 * H) * 2;
+        *reinterpret_cast<uint16_t*>(pg + kScale + si) = static_cast<uint16_t>(d);
+        if constexpr (FMT == KVATTN_FMT_Q4_1) *reinterpret_cast<uint16_t*>(pg + kV41MinOffset + si) = static_cast<uint16_t>(m);
+      }
+      if constexpr (v8) {
+        const uint32_t lo = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, hi = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
+        // lane (token, t') holds channels 8t' + 0..3 in lo and + 4..7 in hi; R / 4 picks one
+#pragma unroll
+        for (int x16 = 0; x16 < 2; ++x16) {
+          uint32_t by[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int from = 4 * (2 * t + (y & 1)) + 2 * x16 + (y >> 1);
+            const uint32_t a = __shfl_sync(0xffffffffu, lo, from), b2 = __shfl_sync(0xffffffffu, hi, from);
+            by[y] = prmt(g >= 4 ? b2 : a, 0u, pick);
+          }
+          w[e][2 * x16 + H] = prmt(prmt(by[0], by[1], 0x0040u), prmt(by[2], by[3], 0x0040u), 0x5410u);
+        }
+      } else {
+        // eight 4-bit codes; with the neighbour's (channels + 8), lane t makes the bytes of channel
+        // group t / 2, elements 4 (t % 2) .. + 3: low nibble channel 16 (t / 2) + e, high + 8
+        uint32_t own = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own |= q[i] << (4 * i);
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+        const uint32_t half = (t & 1) * 16;
+        const uint32_t lo = ((t & 1) ? other : own) >> half, hi = ((t & 1) ? own : other) >> half;
+        // four nibbles over four bytes
+        auto spread = [](uint32_t v) {
+          v = (v & 0xFFu) | ((v & 0xFF00u) << 8);
+          return (v & 0x000F000Fu) | ((v & 0x00F000F0u) << 4);
+        };
+        const uint32_t word = spread(lo) | spread(hi) << 4;
+        // bytes of (2T, x16 = 0), (2T, 1), (2T + 1, 0), (2T + 1, 1) for element R
+        const uint32_t b0 = __shfl_sync(0xffffffffu, word, src), b1 = __shfl_sync(0xffffffffu, word, src + 2);
+        const uint32_t b2 = __shfl_sync(0xffffffffu, word, src + 4), b3 = __shfl_sync(0xffffffffu, word, src + 6);
+        const uint32_t sel = pick | (pick + 4) << 4;
+        w[e][H] = prmt(prmt(b0, b1, sel), prmt(b2, b3, sel), 0x5410u);
+      }
+    }
+  }
+  if constexpr (v8) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<uint4*>(pg + G * 4096 + (((2 * C + e) * 8 + g) * 4 + t) * 16) =
+          make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+  } else {
+    *reinterpret_cast<uint4*>(pg + G * 2048 + ((C * 8 + g) * 4 + t) * 16) = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+  }
+}
+
+// The warp's share of the grid: quarter of the tile, head, tile slot.
+__device__ __forceinline__ bool locate_share(const BatchParams& p, int lane, int* quarter, int* h, TileRows* tr) {
+  const long long item = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  *quarter = static_cast<int>(item & 3);
+  *h = static_cast<int>((item >> 2) % p.n_kv);
+  return locate_tile(p, (item >> 2) / p.n_kv, *h, lane, tr);
 }
 
 template <typename T>
@@ -91,16 +234,180 @@ __global__ void __launch_bounds__(256) append_batch_kernel(const BatchParams p, 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int row = static_cast<int>(item / p.n_kv), h = static_cast<int>(item % p.n_kv);
-  if (row >= p.n_rows) return;
-  int page, slot;
-  if (!locate_row(p, row, h, lane, &page, &slot) || page < 0) return;
-  float kx[8], vx[8];
-  load8<T>(k.data, row * k.row_stride + h * k.head_stride + lane * 8, kx);
-  load8<T>(v.data, row * v.row_stride + h * v.head_stride + lane * 8, vx);
-  encode_token(kx, vx, lane, p.k_pool + page * p.k_stride, p.v_pool + page * p.v_stride, slot, k_fmt, v_fmt,
-               0xffffffffu);
+  int part, h;
+  TileRows tr;
+  if (!locate_share(p, lane, &part, &h, &tr) || tr.page < 0) return;
+  uint8_t* kpg = p.k_pool + tr.page * p.k_stride;
+  uint8_t* vpg = p.v_pool + tr.page * p.v_stride;
+  const T* kr = static_cast<const T*>(k.data) + tr.r0 * k.row_stride + h * k.head_stride;
+  const T* vr = static_cast<const T*>(v.data) + tr.r0 * v.row_stride + h * v.head_stride;
+  if (tr.n == 16) {
+    const int G = tr.slot >> 4;
+    switch (k_fmt) {
+      case kKeyQ8: write_keys<T, KVATTN_FMT_Q8_0>(kr, k.row_stride, kpg, G, part, lane); break;
+      case kKeyQ4: write_keys<T, KVATTN_FMT_Q4_0>(kr, k.row_stride, kpg, G, part, lane); break;
+      case kKeyQ51: write_keys<T, KVATTN_FMT_Q5_1>(kr, k.row_stride, kpg, G, part, lane); break;
+      default: write_keys<T, KVATTN_FMT_Q5_0>(kr, k.row_stride, kpg, G, part, lane); break;
+    }
+    switch (v_fmt) {
+      case kValQ4: write_values<T, KVATTN_FMT_Q4_0>(vr, v.row_stride, vpg, G, part, lane); break;
+      case kValQ8: write_values<T, KVATTN_FMT_Q8_0>(vr, v.row_stride, vpg, G, part, lane); break;
+      default: write_values<T, KVATTN_FMT_Q4_1>(vr, v.row_stride, vpg, G, part, lane); break;
+    }
+    return;
+  }
+  // part of a tile: the four warps take its tokens in turn
+#pragma unroll 1
+  for (int i = part; i < tr.n; i += 4) {
+    float kx[8], vx[8];
+    load8<T>(kr, i * k.row_stride + lane * 8, kx);
+    load8<T>(vr, i * v.row_stride + lane * 8, vx);
+    encode_token(kx, vx, lane, kpg, vpg, tr.slot + i, k_fmt, v_fmt, 0xffffffffu);
+  }
+}
+
+// ------------------------------------------------------------------------------ reading
+// Stores a quad's 32 channels of one row, 8 per lane, in whole 32-byte sectors: fp32 lanes exchange
+// halves with their neighbour first, so that each of the two stores covers full sectors.
+template <typename T>
+__device__ __forceinline__ void store_quad8(T* row, int t, const float (&x)[8], bool live) {
+  if constexpr (sizeof(T) == 4) {
+    const bool odd = t & 1;
+    float4 a, b;
+    float* pa = &a.x;
+    float* pb = &b.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[4 + e], 1);
+      pa[e] = odd ? got : x[e];      // first store: the even lane's eight channels
+      pb[e] = odd ? x[4 + e] : got;  // second store: the odd lane's
+    }
+    if (live) {
+      float* at = reinterpret_cast<float*>(row) + 8 * (t & 2) + 4 * odd;
+      *reinterpret_cast<float4*>(at) = a;
+      *reinterpret_cast<float4*>(at + 8) = b;
+    }
+  } else {
+    if (live) store8<T>(row, 8 * t, x);
+  }
+}
+
+// Channels 64 P .. + 63 of the tile's rows [lo, lo + n).
+template <typename T, int FMT>
+__device__ __forceinline__ void read_keys(T* rows, long long row_stride, const uint8_t* pg, int G, int P, int lane,
+                                          int lo, int n) {
+  const int g = lane >> 2, t = lane & 3;
+  constexpr bool k8 = FMT == KVATTN_FMT_Q8_0, k5 = FMT == KVATTN_FMT_Q5_0 || FMT == KVATTN_FMT_Q5_1;
+  constexpr int kScale = k8 ? kKScaleOffset : k5 ? kK5ScaleOffset : kK4ScaleOffset;
+  uint4 w[2];
+  uint32_t d[2], m[2] = {0u, 0u}, high[2] = {0u, 0u};
+#pragma unroll
+  for (int H = 0; H < 2; ++H) {
+    if constexpr (k8) {
+      w[H] = *reinterpret_cast<const uint4*>(pg + G * 4096 + (((P * 2 + H) * 8 + g) * 4 + t) * 16);
+    } else {
+      const int line = (((P >> 1) * 2 + H) * 8 + g) * 4 + t;
+      const uint2 u = *reinterpret_cast<const uint2*>(pg + G * 2048 + 16 * line + 8 * (P & 1));
+      w[H] = make_uint4(u.x, u.y, 0u, 0u);
+      if constexpr (k5)
+        high[H] = *reinterpret_cast<const uint32_t*>(pg + kK5HighOffset + G * 512 + 4 * line) >> (8 * (P & 1));
+    }
+    const int si = G * 256 + ((g * 2 + H) * 8 + 2 * P) * 2;
+    d[H] = *reinterpret_cast<const uint32_t*>(pg + kScale + si);
+    if constexpr (FMT == KVATTN_FMT_Q5_1) m[H] = *reinterpret_cast<const uint32_t*>(pg + kK5MinOffset + si);
+  }
+#pragma unroll
+  for (int H = 0; H < 2; ++H) {
+    const int row = 8 * H + g;
+    const bool live = row >= lo && row < lo + n;
+    T* to = rows + row * row_stride + 64 * P;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float db = c ? half_hi(d[H]) : half_lo(d[H]);
+      float x[8];
+      if constexpr (k8) {
+        const uint32_t a = c ? w[H].z : w[H].x, b = c ? w[H].w : w[H].y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[e] = static_cast<float>(static_cast<int>(((e < 4 ? a : b) >> (8 * (e & 3))) & 255u) - 128) * db;
+      } else {
+        const uint32_t a = c ? w[H].y : w[H].x;
+        const float mb = c ? half_hi(m[H]) : half_lo(m[H]);
+        constexpr int kOff = FMT == KVATTN_FMT_Q4_0 ? 8 : FMT == KVATTN_FMT_Q5_0 ? 16 : 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t q = (a >> (4 * (e >> 1) + 16 * (e & 1))) & 15u;
+          if constexpr (k5) q |= ((high[H] >> (16 * (e & 1) + 4 * c + (e >> 1))) & 1u) << 4;
+          const float v = static_cast<float>(static_cast<int>(q) - kOff);
+          x[e] = FMT == KVATTN_FMT_Q5_1 ? fmaf(v, db, mb) : v * db;
+        }
+      }
+      store_quad8<T>(to + 32 * c, t, x, live);
+    }
+  }
+}
+
+// Values come as channels R, R + 8, ... of four tokens a lane; they go through the warp's shared
+// rows (16 x 32 channels, a block at a time) to be stored along the channels.
+constexpr int kReadStride = 36;  // floats: lane (R, T) writes bank 8T + R (+ const), lane (g, t) reads 16 bytes
+
+template <typename T, int FMT>
+__device__ __forceinline__ void read_values(T* rows, long long row_stride, const uint8_t* pg, int G, int C, int lane,
+                                            int lo, int n, float* buf) {
+  const int g = lane >> 2, t = lane & 3;  // as the page's lane: R = g, T = t
+  constexpr bool v8 = FMT == KVATTN_FMT_Q8_0;
+  constexpr int kScale = v8 ? kV8ScaleOffset : kV4ScaleOffset;
+  uint4 w[2];
+  uint2 d[2], m[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (v8 || e == 0)
+      w[e] = *reinterpret_cast<const uint4*>(pg + G * (v8 ? 4096 : 2048) + (((v8 ? 2 * C + e : C) * 8 + g) * 4 + t) * 16);
+    d[e] = *reinterpret_cast<const uint2*>(pg + kScale + G * 256 + (t * 8 + 2 * C + e) * 8);
+    if constexpr (FMT == KVATTN_FMT_Q4_1)
+      m[e] = *reinterpret_cast<const uint2*>(pg + kV41MinOffset + G * 256 + (t * 8 + 2 * C + e) * 8);
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    __syncwarp();
+#pragma unroll
+    for (int H = 0; H < 2; ++H) {
+      const uint32_t dw = H ? d[e].y : d[e].x;
+      const float ds[2] = {half_lo(dw), half_hi(dw)};  // tokens 2T, 2T + 1 (+ 8H)
+      float ms[2] = {0.f, 0.f};
+      if constexpr (FMT == KVATTN_FMT_Q4_1) {
+        const uint32_t mw = H ? m[e].y : m[e].x;
+        ms[0] = half_lo(mw);
+        ms[1] = half_hi(mw);
+      }
+#pragma unroll
+      for (int x16 = 0; x16 < 2; ++x16)
+#pragma unroll
+        for (int x8 = 0; x8 < 2; ++x8)
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+            int q;
+            if constexpr (v8) {
+              const uint32_t word = x16 ? (H ? w[e].w : w[e].z) : (H ? w[e].y : w[e].x);
+              q = static_cast<int>((word >> (8 * (2 * x8 + odd))) & 255u) - 128;
+            } else {
+              const uint32_t word = e ? (H ? w[0].w : w[0].z) : (H ? w[0].y : w[0].x);
+              q = static_cast<int>((word >> (8 * (2 * odd + x16) + 4 * x8)) & 15u) - (FMT == KVATTN_FMT_Q4_0 ? 8 : 0);
+            }
+            buf[(2 * t + odd + 8 * H) * kReadStride + 16 * x16 + 8 * x8 + g] =
+                FMT == KVATTN_FMT_Q4_1 ? fmaf(static_cast<float>(q), ds[odd], ms[odd]) : static_cast<float>(q) * ds[odd];
+          }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int H = 0; H < 2; ++H) {
+      const int row = 8 * H + g;
+      const float4 a = *reinterpret_cast<const float4*>(buf + row * kReadStride + 8 * t);
+      const float4 b = *reinterpret_cast<const float4*>(buf + row * kReadStride + 8 * t + 4);
+      const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      store_quad8<T>(rows + row * row_stride + 32 * (2 * C + e), t, x, row >= lo && row < lo + n);
+    }
+  }
 }
 
 template <typename T>
@@ -108,20 +415,39 @@ __global__ void __launch_bounds__(256) read_batch_kernel(const BatchParams p, co
                                                          int k_fmt, int v_fmt) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ __align__(16) float bufs[8][16 * kReadStride];
   const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int row = static_cast<int>(item / p.n_kv), h = static_cast<int>(item % p.n_kv);
-  if (row >= p.n_rows) return;
-  int page, slot;
-  if (!locate_row(p, row, h, lane, &page, &slot)) return;
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  int part, h;
+  TileRows tr;
+  if (!locate_share(p, lane, &part, &h, &tr)) return;
+  const int G = tr.slot >> 4, lo = tr.slot & 15;
+  T* kr = static_cast<T*>(k.data) + (tr.r0 - lo) * k.row_stride + h * k.head_stride;  // row of the tile's first token
+  T* vr = static_cast<T*>(v.data) + (tr.r0 - lo) * v.row_stride + h * v.head_stride;
+  if (tr.page < 0) {
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i = lo + part; i < lo + tr.n; i += 4) {
+      if (k.data) store8<T>(kr, i * k.row_stride + 8 * lane, zero);
+      if (v.data) store8<T>(vr, i * v.row_stride + 8 * lane, zero);
+    }
+    return;
+  }
+  const uint8_t* kpg = p.k_pool + tr.page * p.k_stride;
+  const uint8_t* vpg = p.v_pool + tr.page * p.v_stride;
   if (k.data) {
-    if (page >= 0) decode_key8(p.k_pool + page * p.k_stride, slot, lane, k_fmt, x);
-    store8<T>(k.data, row * k.row_stride + h * k.head_stride + lane * 8, x);
+    switch (k_fmt) {
+      case kKeyQ8: read_keys<T, KVATTN_FMT_Q8_0>(kr, k.row_stride, kpg, G, part, lane, lo, tr.n); break;
+      case kKeyQ4: read_keys<T, KVATTN_FMT_Q4_0>(kr, k.row_stride, kpg, G, part, lane, lo, tr.n); break;
+      case kKeyQ51: read_keys<T, KVATTN_FMT_Q5_1>(kr, k.row_stride, kpg, G, part, lane, lo, tr.n); break;
+      default: read_keys<T, KVATTN_FMT_Q5_0>(kr, k.row_stride, kpg, G, part, lane, lo, tr.n); break;
+    }
   }
   if (v.data) {
-    if (page >= 0) decode_val8(p.v_pool + page * p.v_stride, slot, lane, v_fmt, x);
-    store8<T>(v.data, row * v.row_stride + h * v.head_stride + lane * 8, x);
+    float* buf = bufs[threadIdx.x >> 5];
+    switch (v_fmt) {
+      case kValQ4: read_values<T, KVATTN_FMT_Q4_0>(vr, v.row_stride, vpg, G, part, lane, lo, tr.n, buf); break;
+      case kValQ8: read_values<T, KVATTN_FMT_Q8_0>(vr, v.row_stride, vpg, G, part, lane, lo, tr.n, buf); break;
+      default: read_values<T, KVATTN_FMT_Q4_1>(vr, v.row_stride, vpg, G, part, lane, lo, tr.n, buf); break;
+    }
   }
 }
 
@@ -129,7 +455,7 @@ using RowsKernel = void (*)(BatchParams, RowsView, RowsView, int, int);
 
 static cudaError_t launch_rows(RowsKernel kernel, const BatchParams& p, const RowsView& k, const RowsView& v,
                                int k_fmt, int v_fmt, cudaStream_t stream) {
-  const long long items = p.n_rows * p.n_kv;
+  const long long items = (p.n_rows / 16 + 2ll * p.n_seqs) * p.n_kv * 4;  // tile slots x heads x quarters
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((items + 7) / 8));
   cfg.blockDim = dim3(256);
