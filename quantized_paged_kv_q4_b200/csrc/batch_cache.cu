@@ -19,7 +19,8 @@
 namespace kvattn {
 
 // One warp's share: KV head h, tile `tile` (of the sequence's 16-token tiles) of sequence s, its
-// rows [r0, r0 + n) at slots [slot, slot + n) of page `page` (-1: a bad id).
+// rows [r0, r0 + n) at slots [slot, slot + n) of page `page` (to be checked by page_ok, once other
+// loads are on their way).
 struct TileRows {
   int s, page, slot, n;
   long long r0;
@@ -55,11 +56,13 @@ __device__ __forceinline__ bool locate_tile(const BatchParams& p, long long at, 
   out->n = static_cast<int>(end - first);
   out->r0 = q.r0 + (first - q.pos0);
   out->page = p.page_table[(static_cast<long long>(lo) * p.n_kv + h) * p.max_blocks + first / kPageTokens];
-  if (out->page < 0 || out->page >= p.n_pages) {
-    if (lane == 0) record_error(KVATTN_ERR_BAD_PAGE);
-    out->page = -1;
-  }
   return true;
+}
+
+__device__ __forceinline__ bool page_ok(const BatchParams& p, int page, int lane) {
+  const bool ok = page >= 0 && page < p.n_pages;
+  if (!ok && lane == 0) record_error(KVATTN_ERR_BAD_PAGE);
+  return ok;
 }
 
 // ------------------------------------------------------------------------------ writing
@@ -87,18 +90,23 @@ __device__ __forceinline__ void encode8(const float (&x)[8], int lane, uint32_t 
   *m16 = __half_as_ushort(__float2half_rn(mn));
 }
 
-// Channels 64 P .. + 63 of a whole tile of keys: rows at `rows` (16 of them, row_stride apart), their
-// bytes to the page.
-template <typename T, int FMT>
-__device__ __forceinline__ void write_keys(const T* rows, long long row_stride, uint8_t* pg, int G, int P, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  constexpr bool k8 = FMT == KVATTN_FMT_Q8_0, k5 = FMT == KVATTN_FMT_Q5_0 || FMT == KVATTN_FMT_Q5_1;
-  constexpr int kScale = k8 ? kKScaleOffset : k5 ? kK5ScaleOffset : kK4ScaleOffset;
-  Raw8<T> raw[2][2];
+// The rows of a quarter tile, as every lane takes them: row 8H + g, channels 64 part + 32e + 8t ...
+template <typename T>
+__device__ __forceinline__ void load_quarter(const T* rows, long long row_stride, int part, int lane,
+                                             Raw8<T> (&raw)[2][2]) {
 #pragma unroll
   for (int H = 0; H < 2; ++H)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) raw[H][e] = load_raw8<T>(rows + (8 * H + g) * row_stride, 64 * P + 32 * e + 8 * t);
+    for (int e = 0; e < 2; ++e)
+      raw[H][e] = load_raw8<T>(rows + (8 * H + (lane >> 2)) * row_stride, 64 * part + 32 * e + 8 * (lane & 3));
+}
+
+// Channels 64 P .. + 63 of a whole tile of keys, to their bytes of the page.
+template <typename T, int FMT>
+__device__ __forceinline__ void write_keys(const Raw8<T> (&raw)[2][2], uint8_t* pg, int G, int P, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  constexpr bool k8 = FMT == KVATTN_FMT_Q8_0, k5 = FMT == KVATTN_FMT_Q5_0 || FMT == KVATTN_FMT_Q5_1;
+  constexpr int kScale = k8 ? kKScaleOffset : k5 ? kK5ScaleOffset : kK4ScaleOffset;
 #pragma unroll
   for (int H = 0; H < 2; ++H) {
     uint32_t q[2][8], d[2], m[2];
@@ -147,17 +155,12 @@ __device__ __forceinline__ void write_keys(const T* rows, long long row_stride, 
 // + e; lane (R, T) stores, per block, the codes of channels R, R + 8, R + 16, R + 24 of tokens 2T,
 // 2T + 1 (and + 8).
 template <typename T, int FMT>
-__device__ __forceinline__ void write_values(const T* rows, long long row_stride, uint8_t* pg, int G, int C, int lane) {
+__device__ __forceinline__ void write_values(const Raw8<T> (&raw)[2][2], uint8_t* pg, int G, int C, int lane) {
   const int g = lane >> 2, t = lane & 3;  // as a source; as a target R = g, T = t
   constexpr bool v8 = FMT == KVATTN_FMT_Q8_0;
   constexpr int kScale = v8 ? kV8ScaleOffset : kV4ScaleOffset;
   const int src = 8 * t + (g >> 2);  // lane (token 2T, channel group R / 4)
   const uint32_t pick = g & 3;       // byte R % 4 of its word
-  Raw8<T> raw[2][2];
-#pragma unroll
-  for (int H = 0; H < 2; ++H)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) raw[H][e] = load_raw8<T>(rows + (8 * H + g) * row_stride, 64 * C + 32 * e + 8 * t);
   uint32_t w[2][4];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -236,32 +239,38 @@ __global__ void __launch_bounds__(256) append_batch_kernel(const BatchParams p, 
   const int lane = threadIdx.x & 31;
   int part, h;
   TileRows tr;
-  if (!locate_share(p, lane, &part, &h, &tr) || tr.page < 0) return;
-  uint8_t* kpg = p.k_pool + tr.page * p.k_stride;
-  uint8_t* vpg = p.v_pool + tr.page * p.v_stride;
+  if (!locate_share(p, lane, &part, &h, &tr)) return;
   const T* kr = static_cast<const T*>(k.data) + tr.r0 * k.row_stride + h * k.head_stride;
   const T* vr = static_cast<const T*>(v.data) + tr.r0 * v.row_stride + h * v.head_stride;
+  uint8_t* kpg = p.k_pool + tr.page * p.k_stride;
+  uint8_t* vpg = p.v_pool + tr.page * p.v_stride;
   if (tr.n == 16) {
     const int G = tr.slot >> 4;
+    Raw8<T> kraw[2][2], vraw[2][2];
+    load_quarter(kr, k.row_stride, part, lane, kraw);
+    load_quarter(vr, v.row_stride, part, lane, vraw);
+    if (!page_ok(p, tr.page, lane)) return;
     switch (k_fmt) {
-      case kKeyQ8: write_keys<T, KVATTN_FMT_Q8_0>(kr, k.row_stride, kpg, G, part, lane); break;
-      case kKeyQ4: write_keys<T, KVATTN_FMT_Q4_0>(kr, k.row_stride, kpg, G, part, lane); break;
-      case kKeyQ51: write_keys<T, KVATTN_FMT_Q5_1>(kr, k.row_stride, kpg, G, part, lane); break;
-      default: write_keys<T, KVATTN_FMT_Q5_0>(kr, k.row_stride, kpg, G, part, lane); break;
+      case kKeyQ8: write_keys<T, KVATTN_FMT_Q8_0>(kraw, kpg, G, part, lane); break;
+      case kKeyQ4: write_keys<T, KVATTN_FMT_Q4_0>(kraw, kpg, G, part, lane); break;
+      case kKeyQ51: write_keys<T, KVATTN_FMT_Q5_1>(kraw, kpg, G, part, lane); break;
+      default: write_keys<T, KVATTN_FMT_Q5_0>(kraw, kpg, G, part, lane); break;
     }
     switch (v_fmt) {
-      case kValQ4: write_values<T, KVATTN_FMT_Q4_0>(vr, v.row_stride, vpg, G, part, lane); break;
-      case kValQ8: write_values<T, KVATTN_FMT_Q8_0>(vr, v.row_stride, vpg, G, part, lane); break;
-      default: write_values<T, KVATTN_FMT_Q4_1>(vr, v.row_stride, vpg, G, part, lane); break;
+      case kValQ4: write_values<T, KVATTN_FMT_Q4_0>(vraw, vpg, G, part, lane); break;
+      case kValQ8: write_values<T, KVATTN_FMT_Q8_0>(vraw, vpg, G, part, lane); break;
+      default: write_values<T, KVATTN_FMT_Q4_1>(vraw, vpg, G, part, lane); break;
     }
     return;
   }
   // part of a tile: the four warps take its tokens in turn
 #pragma unroll 1
   for (int i = part; i < tr.n; i += 4) {
+    const Raw8<T> kraw = load_raw8<T>(kr, i * k.row_stride + lane * 8), vraw = load_raw8<T>(vr, i * v.row_stride + lane * 8);
+    if (!page_ok(p, tr.page, lane)) return;
     float kx[8], vx[8];
-    load8<T>(kr, i * k.row_stride + lane * 8, kx);
-    load8<T>(vr, i * v.row_stride + lane * 8, vx);
+    widen8<T>(kraw, kx);
+    widen8<T>(vraw, vx);
     encode_token(kx, vx, lane, kpg, vpg, tr.slot + i, k_fmt, v_fmt, 0xffffffffu);
   }
 }
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(256) read_batch_kernel(const BatchParams p, co
   const int G = tr.slot >> 4, lo = tr.slot & 15;
   T* kr = static_cast<T*>(k.data) + (tr.r0 - lo) * k.row_stride + h * k.head_stride;  // row of the tile's first token
   T* vr = static_cast<T*>(v.data) + (tr.r0 - lo) * v.row_stride + h * v.head_stride;
-  if (tr.page < 0) {
+  if (!page_ok(p, tr.page, lane)) {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int i = lo + part; i < lo + tr.n; i += 4) {
       if (k.data) store8<T>(kr, i * k.row_stride + 8 * lane, zero);
