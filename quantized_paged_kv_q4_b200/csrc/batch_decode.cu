@@ -3,12 +3,17 @@
 // tokens and verify batches).
 //
 // A unit is one (sequence, KV head): its query rows (group x rows <= 24) against its 16-token
-// tiles.  A warp group (one warp per 8 query rows) works by itself: it streams its own tiles
-// through its own ring of stages, keeps its own softmax state and writes its own results.  No
-// group waits for another, so what a unit costs beside its tiles (query fragments, output) hides
-// behind the arithmetic of the SM's other groups, and the ring runs on from one unit into the
-// next.  The copies are 16 bytes a lane (cp.async): a tile has four to six short regions, and a
-// bulk copy of each, issued by the warp that also computes, took 700 of the 3,400 cycles a tile.
+// tiles.  A group of warps works by itself: it streams its own tiles through its own ring of
+// stages, keeps its own softmax state and writes its own results.  No group waits for another, so
+// what a unit costs beside its tiles (query fragments, output) hides behind the arithmetic of the
+// SM's other groups, and the ring runs on from one unit into the next.  The copies are 16 bytes a
+// lane (cp.async): a tile has four to six short regions, and a bulk copy of each, issued by the
+// warp that also computes, took 700 of the 3,400 cycles a tile.
+//
+// Up to 8 query rows (one n-tile) a group is one warp (decode_batch_kernel).  With 9 to 24 rows it
+// is four (decode_batch_wide_kernel): each takes the scores of one tile of a step of four, for all
+// rows, and then a quarter of the channels of all four tiles' values, so that every code is
+// decoded once, not once per n-tile; P goes between them through shared memory.
 //
 // All units form one line, each as long as its tiles and what it costs beside them (kUnitCost),
 // and every group takes an equal stretch of it, whatever the lengths are: a group may hold the end
@@ -19,9 +24,10 @@
 // a fixed order.  A group has at most two partials, its first unit's and its last's, so the
 // workspace has two slots per group.
 //
-// An earlier arrangement gave a CTA of four groups one stretch and merged the groups' states
-// through shared memory at the end of each unit: 2 to 4 us of barriers per unit (32 ragged
-// sequences of up to 16,384 tokens: 51.9 us).
+// Not kept: a CTA of four groups on one stretch, their states merged through shared memory at the
+// end of each unit (2 to 4 us of barriers a unit: 32 ragged sequences of up to 16,384 tokens in
+// 51.9 us, against 40.4); three warps per tile with 24 rows, one per n-tile (eight verify steps of
+// four tokens in 81 us).
 #include <algorithm>
 
 #include "batch.cuh"
@@ -58,10 +64,11 @@ struct BatchUnit {
 
 // What a warp's copying keeps between two tiles, in shared memory (registers are the tile's): the
 // unit of the next tile, where that starts in the group's numbering, the positions its rows see,
-// and the page at hand: its first position (-1: nothing of it is fetched) and its bytes.
+// and either the page at hand (its first position, -1: nothing of it is fetched, and its bytes) or
+// the next step's first tile.
 struct alignas(16) Producer {
   int unit, start, t0, n;
-  int last, low, key0, pad;
+  int last, low, key0, next;
   const uint8_t *k, *v;
 };
 
@@ -76,33 +83,65 @@ struct alignas(16) BatchPlanState {
   Producer producer[WARPS];
 };
 
-template <int KF, int VF, int NT, typename T>
+constexpr int kBatchRoom = 224 * 1024;  // of shared memory, for rings, fragments and P; 3 KB for the plan
+constexpr int kBatchMeta = 3 * 1024;
+
+// One CTA per SM, of as many groups (warps) as shared memory holds with two stages each, up to
+// twelve (three per scheduler, 168 registers a thread); then as many stages as fit, up to 6.
+template <int KF, int VF, typename T>
 struct BatchCfg {
-  using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
-  static constexpr int kRowsPad = NT * 8;
+  static constexpr int kRowsPad = 8;
   static constexpr int kTileBytes = L::kBytes;
-  // the query's B fragments: [n-tile][block][k-step][lane]
+  // the query's B fragments: [block][k-step][lane]
   static constexpr int kQFragBytes = BatchParts<T>::kQ == 2 ? 16 : 8;
-  static constexpr int kQWarpBytes = 16 * 32 * kQFragBytes;
-  static constexpr int kMeta = 3 * 1024;  // the plan and the tiles' positions
-  // One CTA per SM, of as many groups as shared memory holds with two stages each, up to twelve
-  // warps (three per scheduler, 168 registers a thread); then as many stages as fit, up to 6.
-  static constexpr int kRoom = 227 * 1024 - kMeta;
-  static constexpr int kFit = kRoom / (NT * kQWarpBytes + 2 * kTileBytes);
-  static constexpr int kGroups = kFit < 12 / NT ? kFit : 12 / NT;
-  static constexpr int kStagesFit = (kRoom / kGroups - NT * kQWarpBytes) / kTileBytes;
+  static constexpr int kQBytes = 16 * 32 * kQFragBytes;
+  static constexpr int kFit = kBatchRoom / (kQBytes + 2 * kTileBytes);
+  static constexpr int kGroups = kFit < 12 ? kFit : 12;
+  static constexpr int kStagesFit = (kBatchRoom / kGroups - kQBytes) / kTileBytes;
   static constexpr int kStages = kStagesFit < 6 ? kStagesFit : 6;
-  static constexpr int kWarps = kGroups * NT;
+  static constexpr int kWarps = kGroups;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kQOff = kGroups * kStages * kTileBytes;
-  static constexpr int kMetaOff = kQOff + kWarps * kQWarpBytes;
-  static constexpr int kSmemBytes = kMetaOff + kMeta;
-  static_assert(kStages >= 2 && kSmemBytes <= 227 * 1024, "shared memory");
-  static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kMeta, "meta");
-  static_assert(kMetaOff % 16 == 0 && kQOff % 16 == 0 && sizeof(BatchPlanState<kWarps, kGroups>) % 16 == 0, "alignment");
+  static constexpr int kGroupBytes = kStages * kTileBytes + kQBytes;
+  static constexpr int kMetaOff = kGroups * kGroupBytes;
+  static constexpr int kSmemBytes = kMetaOff + kBatchMeta;
+  static_assert(kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
+  static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
   // What a unit costs beside its tiles, and the least a group takes, in tiles.
   static constexpr int kUnitCost = 2, kMinShare = 4;
+};
+
+// The wide kernel's state of a unit, per group: rows in order.
+template <int NR>
+struct alignas(16) WideState {
+  float crow[8 * NR];
+  int qpos[8 * NR];
+  float top[4][8 * NR], sum[4][8 * NR];  // of each warp
+  uint2 qsums[NR][32];                   // zero-point keys: block sums as B fragments
+};
+
+template <int KF, int VF, int NR, typename T>
+struct WideCfg {
+  using L = SingleTileLayout<KF, VF>;
+  static constexpr int kRowsPad = 8 * NR;
+  static constexpr int kTileBytes = L::kBytes;
+  static constexpr int kQFragBytes = BatchParts<T>::kQ == 2 ? 16 : 8, kPFragBytes = BatchParts<T>::kP == 2 ? 16 : 8;
+  static constexpr int kQTileBytes = 16 * 32 * kQFragBytes;   // of one n-tile
+  static constexpr int kPTileBytes = NR * 32 * kPFragBytes;   // of one tile of tokens
+  static constexpr int kFixed = NR * kQTileBytes + 4 * kPTileBytes + sizeof(WideState<NR>);
+  static constexpr int kStepBytes = 4 * kTileBytes;
+  static constexpr int kFit = kBatchRoom / (kFixed + 2 * kStepBytes);
+  static constexpr int kGroups = kFit < 3 ? kFit : 3;
+  static constexpr int kStagesFit = (kBatchRoom / kGroups - kFixed) / kStepBytes;
+  static constexpr int kStages = kStagesFit < 4 ? kStagesFit : 4;
+  static constexpr int kWarps = 4 * kGroups;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kGroupBytes = kStages * kStepBytes + kFixed;
+  static constexpr int kMetaOff = kGroups * kGroupBytes;
+  static constexpr int kSmemBytes = kMetaOff + kBatchMeta;
+  static_assert(kGroups >= 1 && kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
+  static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
+  static constexpr int kUnitCost = 6, kMinShare = 8;
 };
 
 __device__ __forceinline__ int lds_int(const int* p) { return static_cast<int>(lds32(smem_u32(p))); }
@@ -175,136 +214,244 @@ __device__ __forceinline__ void cp16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
-template <int KF, int VF, int NT, typename T>
-__global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_batch_kernel(const BatchDecodeParams p) {
-  using C = BatchCfg<KF, VF, NT, T>;
+// The groups' stretches of the line of all units, into shared memory; false: the CTA has none.
+template <typename C>
+__device__ __forceinline__ bool plan_stretches(const BatchDecodeParams& p, BatchPlanState<C::kWarps, C::kGroups>* plan) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.b.n_seqs + C::kThreads - 1) / C::kThreads;
+  const int s0 = min(static_cast<int>(threadIdx.x) * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
+  int tiles = 0, units = 0;  // of this thread's sequences (the host keeps the whole line below 2^31)
+  BatchSeq seq{};            // the last of them (the only one, with few sequences)
+  int n_seq = 0;             // its tiles per unit, without n_list
+  for (int s = s0; s < s1; ++s) {
+    seq = load_decode_seq(p, s);
+    if (seq.rows == 0) continue;
+    units += p.b.n_kv;
+    if (p.n_list) {
+      for (int h = 0; h < p.b.n_kv; ++h) tiles += unit_tiles(p, seq, static_cast<long long>(s) * p.b.n_kv + h);
+    } else {
+      n_seq = unit_tiles(p, seq, 0);
+      tiles += p.b.n_kv * n_seq;
+    }
+  }
+  int t_end = tiles, u_end = units;  // inclusive sums over the warp, then the block
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, t_end, d), b = __shfl_up_sync(0xffffffffu, u_end, d);
+    if (lane >= d) t_end += a, u_end += b;
+  }
+  if (lane == 31) plan->tiles[warp] = t_end, plan->units[warp] = u_end;
+  __syncthreads();
+  int t_all = 0, u_all = 0;
+#pragma unroll
+  for (int w = 0; w < C::kWarps; ++w) {
+    if (w < warp) t_end += plan->tiles[w], u_end += plan->units[w];
+    t_all += plan->tiles[w], u_all += plan->units[w];
+  }
+  const int all = t_all + C::kUnitCost * u_all, takers = static_cast<int>(gridDim.x) * C::kGroups;
+  const int share = max((all + takers - 1) / takers, C::kMinShare);
+  // Stretch i gridDim.x + blockIdx.x is group i's: the first ones go to different SMs.
+  const int stride = share * static_cast<int>(gridDim.x), base = share * static_cast<int>(blockIdx.x);
+  if (base >= all) return false;
+  if (threadIdx.x < C::kGroups) {
+    const long long from = base + static_cast<long long>(threadIdx.x) * stride;
+    if (from >= all) plan->from[threadIdx.x] = t_all;
+    if (from + share >= all) plan->to[threadIdx.x] = t_all;
+  }
+  // Every end belongs to the thread whose sequences hold it: end e (0: a stretch's start, 1: its
+  // end) of group i sits at base + e share + i stride.
+  int at = t_end + C::kUnitCost * u_end - tiles - C::kUnitCost * units, before = t_end - tiles;
+  for (int s = s0; s < s1 && units > 0; ++s) {
+    if (per > 1) {
+      seq = load_decode_seq(p, s);
+      if (seq.rows == 0) continue;
+      if (!p.n_list) n_seq = unit_tiles(p, seq, 0);
+    }
+    // units of one length are passed in one go, units with lists one by one
+    const int step = p.n_list ? 1 : p.b.n_kv;
+    for (int h0 = 0; h0 < p.b.n_kv; h0 += step) {
+      const int n = p.n_list ? unit_tiles(p, seq, static_cast<long long>(s) * p.b.n_kv + h0) : n_seq;
+      const int len = C::kUnitCost + n, end = at + step * len;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int off = base + e * share;
+        int i = at <= off ? 0 : (at - off + stride - 1) / stride;  // the group's first end not before `at`
+        for (; i < C::kGroups && off + static_cast<long long>(i) * stride < end; ++i) {
+          const int in = off + i * stride - at, hh = in / len, skip = max(in - hh * len - C::kUnitCost, 0);
+          if (e == 1) {
+            plan->to[i] = before + hh * n + skip;
+          } else {
+            const int h = h0 + hh;
+            plan->from[i] = before + hh * n + skip;
+            plan->skip[i] = skip;
+            plan->unit[i] =
+                BatchUnit{s * p.b.n_kv + h, h, seq.r0, seq.rows, seq.pos0, seq_first_tile(p, seq), n};
+          }
+        }
+      }
+      at = end;
+      before += step * n;
+    }
+  }
+  __syncthreads();
+  return true;
+}
+
+// The B fragments of query rows 8 nt .. + 7 of the unit, to shared memory (one warp).  A row is scaled by
+// the power of two that puts its largest magnitude into [1, 2) (exact), and split into f16 parts.
+// Returns what turns a dot product with scaled row g into a base-2 score; zero-point keys: the
+// rows' block sums as a B fragment.  `between` runs while the rows are on their way.
+template <typename T, int QP, bool KMIN, typename Between>
+__device__ __forceinline__ float query_fragments(const BatchDecodeParams& p, const BatchUnit& un, int nt, int lane,
+                                                 uint32_t q_s, uint32_t& qsb_hi, uint32_t& qsb_lo, Between between) {
+  constexpr int kFragBytes = QP == 2 ? 16 : 8;
+  const int g = lane >> 2, t = lane & 3;
+  const int r = nt * 8 + g;
+  Raw8<T> raw[kBlocks];
+  const bool live = r < un.rows * p.group;
+  if (live) {
+    const int qi = r / p.group, jj = r - qi * p.group;
+    const long long at = (un.r0 + qi) * p.q.row_stride + (un.h * p.group + jj) * p.q.head_stride;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) raw[b] = load_raw8<T>(p.q.data, at + 32 * b + 8 * t);
+  }
+  between();
+  float x[kBlocks][8];
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    if (live) {
+      widen8<T>(raw[b], x[b]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[b][e] = 0.f;
+    }
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  // 2^e <= amax < 2^(e+1), kept where both 2^e and 2^-e are normal numbers
+  const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 1), 253);
+  const float inv = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+  float qs0 = 0.f, qs1 = 0.f;
+#pragma unroll
+  for (int bl = 0; bl < kBlocks; ++bl) {
+    float xv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) xv[e] = x[bl][e] * inv;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      uint32_t hi[2], lo[2];
+      split_pair(xv[4 * ks], xv[4 * ks + 1], hi[0], lo[0]);
+      split_pair(xv[4 * ks + 2], xv[4 * ks + 3], hi[1], lo[1]);
+      const uint32_t to = q_s + ((bl * 2 + ks) * 32 + lane) * kFragBytes;
+      if constexpr (QP == 2)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(lo[0]),
+                     "r"(lo[1])
+                     : "memory");
+      else
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(hi[0]), "r"(hi[1]) : "memory");
+    }
+    if constexpr (KMIN) {
+      float sm = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sm += xv[e];
+      sm += __shfl_xor_sync(0xffffffffu, sm, 1);
+      sm += __shfl_xor_sync(0xffffffffu, sm, 2);
+      if (bl == 2 * t) qs0 = sm;
+      if (bl == 2 * t + 1) qs1 = sm;
+    }
+  }
+  if constexpr (KMIN) split_pair(qs0, qs1, qsb_hi, qsb_lo);
+  return __uint_as_float(static_cast<uint32_t>(ex) << 23) * (1.0f / 16.0f) * 1.4426950408889634f;
+}
+
+// Entry i of unit u's list: page (-2: none there) and logical block.
+__device__ __forceinline__ int2 page_of(const BatchDecodeParams& p, int u, int i) {
+  const long long at = static_cast<long long>(u) * p.b.max_blocks + i;
+  const bool any = i < p.b.max_blocks && (!p.n_list || i < p.n_list[u]);
+  return make_int2(any ? p.b.page_table[at] : -2, any && p.page_logical ? p.page_logical[at] : i);
+}
+
+// Makes w the unit of the warp's copying, its first tile at `start`.
+__device__ __forceinline__ void producer_unit(const BatchDecodeParams& p, Producer* prod, const BatchUnit& w, int start,
+                                              int lane) {
+  if (lane == 0) {
+    prod->unit = w.unit;
+    prod->start = start;
+    prod->t0 = w.t0;
+    prod->n = w.n;
+    prod->last = w.pos0 + w.rows - 1;
+    prod->low = p.window > 0 ? max(0, w.pos0 - p.window + 1) : 0;
+  }
+  __syncwarp();
+}
+
+// Whether block e.y with page id e.x holds a key that some row sees (a bad id of such a block is recorded).
+__device__ __forceinline__ bool fetch_block(const BatchDecodeParams& p, int2 e, int last, int low, int lane) {
+  if (e.x == -2 || e.y < 0 || e.y > last / kPageTokens || e.y < low / kPageTokens) return false;
+  if (e.x >= 0 && e.x < p.b.n_pages) return true;
+  if (lane == 0) record_error(KVATTN_ERR_BAD_PAGE);
+  return false;
+}
+
+// Starts the copies of tile G of a page into a stage's tile (one warp, 16 bytes a lane).
+template <int KF, int VF>
+__device__ __forceinline__ void copy_tile(uint32_t to, const uint8_t* k_page, const uint8_t* v_page, int G, int lane) {
+  using F = TileFormat<KF, VF>;
+  using L = SingleTileLayout<KF, VF>;
+  to += 16 * lane;
+  k_page += 16 * lane;
+  v_page += 16 * lane;
+  const uint8_t* src = k_page + G * L::kKCodes;
+#pragma unroll
+  for (int i = 0; i < L::kKCodes; i += 512) cp16(to + i, src + i);
+  if constexpr (F::kK5) cp16(to + L::kKHigh, k_page + kK5HighOffset + G * 512);
+  src = v_page + G * L::kVCodes;
+#pragma unroll
+  for (int i = 0; i < L::kVCodes; i += 512) cp16(to + L::kV + i, src + i);
+  // 256 bytes each: lanes 0-15 the K scales, 16-31 the V scales, then 0-15 the minima
+  const uint8_t* narrow = lane < 16 ? k_page + F::kKScaleOff : v_page + (F::kVScaleOff - 256);
+  cp16(to + L::kSmall, narrow + G * 256);
+  if constexpr (F::kKMin || F::kVMin) {
+    const uint8_t* low = F::kKMin ? k_page + kK5MinOffset : v_page + kV41MinOffset;
+    if (lane < 16) cp16(to + L::kSmall + 512, low + G * 256);
+  }
+}
+
+// ---- up to 8 query rows: one warp per group
+template <int KF, int VF, typename T>
+__global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch_kernel(const BatchDecodeParams p) {
+  using C = BatchCfg<KF, VF, T>;
   using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
   constexpr int QP = BatchParts<T>::kQ, PP = BatchParts<T>::kP;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int grp = warp / NT, nt0 = warp % NT;
   auto* plan = reinterpret_cast<BatchPlanState<C::kWarps, C::kGroups>*>(smem + C::kMetaOff);
   // first position of the tile in each of the warp's stages, -1: none
-  int* key_of = reinterpret_cast<int*>(plan + 1) + warp * C::kStages;
+  int* key_of = reinterpret_cast<int*>(plan + 1) + grp * C::kStages;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // only now, so that the merge grid may read the batch's arrays before this grid is done
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- the plan: the groups' stretches of the line of all units
-  {
-    const int per = (p.b.n_seqs + C::kThreads - 1) / C::kThreads;
-    const int s0 = min(static_cast<int>(threadIdx.x) * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
-    int tiles = 0, units = 0;  // of this thread's sequences (the host keeps the whole line below 2^31)
-    BatchSeq seq{};            // the last of them (the only one, with few sequences)
-    int n_seq = 0;             // its tiles per unit, without n_list
-    for (int s = s0; s < s1; ++s) {
-      seq = load_decode_seq(p, s);
-      if (seq.rows == 0) continue;
-      units += p.b.n_kv;
-      if (p.n_list) {
-        for (int h = 0; h < p.b.n_kv; ++h) tiles += unit_tiles(p, seq, static_cast<long long>(s) * p.b.n_kv + h);
-      } else {
-        n_seq = unit_tiles(p, seq, 0);
-        tiles += p.b.n_kv * n_seq;
-      }
-    }
-    int t_end = tiles, u_end = units;  // inclusive sums over the warp, then the block
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, t_end, d), b = __shfl_up_sync(0xffffffffu, u_end, d);
-      if (lane >= d) t_end += a, u_end += b;
-    }
-    if (lane == 31) plan->tiles[warp] = t_end, plan->units[warp] = u_end;
-    __syncthreads();
-    int t_all = 0, u_all = 0;
-#pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-      if (w < warp) t_end += plan->tiles[w], u_end += plan->units[w];
-      t_all += plan->tiles[w], u_all += plan->units[w];
-    }
-    const int all = t_all + C::kUnitCost * u_all, takers = static_cast<int>(gridDim.x) * C::kGroups;
-    const int share = max((all + takers - 1) / takers, C::kMinShare);
-    // Stretch i gridDim.x + blockIdx.x is group i's: the first ones go to different SMs.
-    const int stride = share * static_cast<int>(gridDim.x), base = share * static_cast<int>(blockIdx.x);
-    if (base >= all) return;  // past the end of the line
-    if (threadIdx.x < C::kGroups) {
-      const long long from = base + static_cast<long long>(threadIdx.x) * stride;
-      if (from >= all) plan->from[threadIdx.x] = t_all;
-      if (from + share >= all) plan->to[threadIdx.x] = t_all;
-    }
-    // Every end belongs to the thread whose sequences hold it: end e (0: a stretch's start, 1: its
-    // end) of group i sits at base + e share + i stride.
-    int at = t_end + C::kUnitCost * u_end - tiles - C::kUnitCost * units, before = t_end - tiles;
-    for (int s = s0; s < s1 && units > 0; ++s) {
-      if (per > 1) {
-        seq = load_decode_seq(p, s);
-        if (seq.rows == 0) continue;
-        if (!p.n_list) n_seq = unit_tiles(p, seq, 0);
-      }
-      // units of one length are passed in one go, units with lists one by one
-      const int step = p.n_list ? 1 : p.b.n_kv;
-      for (int h0 = 0; h0 < p.b.n_kv; h0 += step) {
-        const int n = p.n_list ? unit_tiles(p, seq, static_cast<long long>(s) * p.b.n_kv + h0) : n_seq;
-        const int len = C::kUnitCost + n, end = at + step * len;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int off = base + e * share;
-          int i = at <= off ? 0 : (at - off + stride - 1) / stride;  // the group's first end not before `at`
-          for (; i < C::kGroups && off + static_cast<long long>(i) * stride < end; ++i) {
-            const int in = off + i * stride - at, hh = in / len, skip = max(in - hh * len - C::kUnitCost, 0);
-            if (e == 1) {
-              plan->to[i] = before + hh * n + skip;
-            } else {
-              const int h = h0 + hh;
-              plan->from[i] = before + hh * n + skip;
-              plan->skip[i] = skip;
-              plan->unit[i] =
-                  BatchUnit{s * p.b.n_kv + h, h, seq.r0, seq.rows, seq.pos0, seq_first_tile(p, seq), n};
-            }
-          }
-        }
-        at = end;
-        before += step * n;
-      }
-    }
-    __syncthreads();
-  }
+  if (!plan_stretches<C>(p, plan)) return;
   const int n_tiles = plan->to[grp] - plan->from[grp];
   if (n_tiles <= 0) return;
 
-  // ---- the group's ring: its tile k goes to stage k % kStages.  Every warp of the group keeps the
-  // same account and copies its share of each tile (every NT-th 512 bytes).
-  const uint32_t ring = smem_u32(smem + grp * C::kStages * C::kTileBytes);
-  Producer* prod = &plan->producer[warp];
+  // ---- the group's ring: its tile k goes to stage k % kStages
+  uint8_t* ring = smem + grp * C::kGroupBytes;
+  const uint32_t ring_s = smem_u32(ring), q_s = ring_s + C::kStages * C::kTileBytes;
+  Producer* prod = &plan->producer[grp];
 
-  auto start_unit = [&](const BatchUnit& w, int start) {
-    if (lane == 0) {
-      prod->unit = w.unit;
-      prod->start = start;
-      prod->t0 = w.t0;
-      prod->n = w.n;
-      prod->last = w.pos0 + w.rows - 1;
-      prod->low = p.window > 0 ? max(0, w.pos0 - p.window + 1) : 0;
-    }
-    __syncwarp();
-  };
-  // entry i of unit u's list: page (-2: none there) and logical block
-  auto page_of = [&](int u, int i) -> int2 {
-    const long long at = static_cast<long long>(u) * p.b.max_blocks + i;
-    const bool any = i < p.b.max_blocks && (!p.n_list || i < p.n_list[u]);
-    return make_int2(any ? p.b.page_table[at] : -2, any && p.page_logical ? p.page_logical[at] : i);
-  };
-  // Makes entry `e` the page at hand.  A block that no row sees has nothing to fetch, whatever its id.
+  // makes entry `e` the page at hand
   auto open_page = [&](int2 e) {
-    const int last = lds_int(&prod->last), low = lds_int(&prod->low);
-    bool fetch = e.x != -2 && e.y >= 0 && e.y <= last / kPageTokens && e.y >= low / kPageTokens;
-    if (fetch && (e.x < 0 || e.x >= p.b.n_pages)) {
-      if (lane == 0) record_error(KVATTN_ERR_BAD_PAGE);
-      fetch = false;
-    }
+    const bool fetch = fetch_block(p, e, lds_int(&prod->last), lds_int(&prod->low), lane);
     if (lane == 0) {
       prod->key0 = fetch ? e.y * kPageTokens : -1;
       prod->k = p.b.k_pool + e.x * p.b.k_stride;  // used only when fetched
@@ -322,64 +469,37 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_b
       if (k >= end) {
         __syncwarp();
         const BatchUnit w = next_unit(p, u);
-        start_unit(w, end);
+        producer_unit(p, prod, w, end, lane);
         u = w.unit;
         start = end;
         end += w.n;
         j = w.t0;
-        ahead = page_of(u, j >> 3);
+        ahead = page_of(p, u, j >> 3);
       }
       const int G = j & 7;
       if (k > 0 && (G == 0 || k == start)) {
         open_page(ahead);
-        if (k + 8 - G < end) ahead = page_of(u, (j >> 3) + 1);
+        if (k + 8 - G < end) ahead = page_of(p, u, (j >> 3) + 1);
       }
       const int key0 = lds_int(&prod->key0), key = key0 + 16 * G, st = k % C::kStages;
       const bool fetch = key0 >= 0 && key <= lds_int(&prod->last) && key + 15 >= lds_int(&prod->low);
       if (lane == 0) *reinterpret_cast<volatile int*>(&key_of[st]) = fetch ? key : -1;
-      if (fetch) {
-        const uint8_t* k_page = lds_ptr(&prod->k) + 16 * lane;
-        const uint8_t* v_page = lds_ptr(&prod->v) + 16 * lane;
-        const uint32_t to = ring + st * C::kTileBytes + 16 * lane;
-        int turn = 0;  // constant in the unrolled code
-        auto mine = [&]() { return NT == 1 || turn++ % NT == nt0; };
-        const uint8_t* src = k_page + G * L::kKCodes;
-#pragma unroll
-        for (int i = 0; i < L::kKCodes; i += 512)
-          if (mine()) cp16(to + i, src + i);
-        if constexpr (F::kK5) {
-          if (mine()) cp16(to + L::kKHigh, k_page + kK5HighOffset + G * 512);
-        }
-        src = v_page + G * L::kVCodes;
-#pragma unroll
-        for (int i = 0; i < L::kVCodes; i += 512)
-          if (mine()) cp16(to + L::kV + i, src + i);
-        // 256 bytes each: lanes 0-15 the K scales, 16-31 the V scales, then 0-15 the minima
-        const uint8_t* narrow = lane < 16 ? k_page + F::kKScaleOff : v_page + (F::kVScaleOff - 256);
-        if (mine()) cp16(to + L::kSmall, narrow + G * 256);
-        if constexpr (F::kKMin || F::kVMin) {
-          const uint8_t* low = F::kKMin ? k_page + kK5MinOffset : v_page + kV41MinOffset;
-          if (mine() && lane < 16) cp16(to + L::kSmall + 512, low + G * 256);
-        }
-      }
+      if (fetch) copy_tile<KF, VF>(ring_s + st * C::kTileBytes, lds_ptr(&prod->k), lds_ptr(&prod->v), G, lane);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-  BatchUnit* mine = &plan->at_work[warp];
+  BatchUnit* mine = &plan->at_work[grp];
   int start = -plan->skip[grp];  // first tile of the unit, in the group's numbering
   int k = 0;                     // tiles this group has consumed
-  const uint32_t q_s = smem_u32(smem + C::kQOff + warp * C::kQWarpBytes);  // each warp its own fragments
   if (lane == 0) *mine = plan->unit[grp];
   __syncwarp();
-  start_unit(*mine, start);
+  producer_unit(p, prod, *mine, start, lane);
 
   while (true) {
     const BatchUnit un = *mine;
     const int end = min(start + un.n, n_tiles);  // the group's tiles of the unit: [k, end)
 
-    // ---- the query's fragments.  A row is scaled by the power of two that puts its largest
-    // magnitude into [1, 2) (exact), and split into f16 parts.
     float crow[2];
     uint32_t qsb_hi = 0u, qsb_lo = 0u;
     {
@@ -387,73 +507,15 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_b
       int2 here = make_int2(-2, 0);
       if (k == 0) {
         const int i = (un.t0 - start) >> 3;
-        here = page_of(un.unit, i);
-        ahead = page_of(un.unit, i + 1);
+        here = page_of(p, un.unit, i);
+        ahead = page_of(p, un.unit, i + 1);
       }
-      const int r = nt0 * 8 + g;
-      Raw8<T> raw[kBlocks];
-      const bool live = r < un.rows * p.group;
-      if (live) {
-        const int qi = r / p.group, jj = r - qi * p.group;
-        const long long at = (un.r0 + qi) * p.q.row_stride + (un.h * p.group + jj) * p.q.head_stride;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) raw[b] = load_raw8<T>(p.q.data, at + 32 * b + 8 * t);
-      }
-      if (k == 0) {
-        open_page(here);
-        for (int i = 0; i < C::kStages - (NT > 1); ++i) issue(i);
-      }
-      float x[kBlocks][8];
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        if (live) {
-          widen8<T>(raw[b], x[b]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[b][e] = 0.f;
+      const float cr = query_fragments<T, QP, F::kKMin>(p, un, 0, lane, q_s, qsb_hi, qsb_lo, [&]() {
+        if (k == 0) {
+          open_page(here);
+          for (int i = 0; i < C::kStages; ++i) issue(i);
         }
-      }
-      float amax = 0.f;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^e <= amax < 2^(e+1), kept where both 2^e and 2^-e are normal numbers
-      const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 1), 253);
-      const float inv = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-      float qs0 = 0.f, qs1 = 0.f;
-#pragma unroll
-      for (int bl = 0; bl < kBlocks; ++bl) {
-        float xv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xv[e] = x[bl][e] * inv;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          uint32_t hi[2], lo[2];
-          split_pair(xv[4 * ks], xv[4 * ks + 1], hi[0], lo[0]);
-          split_pair(xv[4 * ks + 2], xv[4 * ks + 3], hi[1], lo[1]);
-          const uint32_t to = q_s + ((bl * 2 + ks) * 32 + lane) * C::kQFragBytes;
-          if constexpr (QP == 2)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(lo[0]),
-                         "r"(lo[1])
-                         : "memory");
-          else
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(hi[0]), "r"(hi[1]) : "memory");
-        }
-        if constexpr (F::kKMin) {
-          float sm = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sm += xv[e];
-          sm += __shfl_xor_sync(0xffffffffu, sm, 1);
-          sm += __shfl_xor_sync(0xffffffffu, sm, 2);
-          if (bl == 2 * t) qs0 = sm;
-          if (bl == 2 * t + 1) qs1 = sm;
-        }
-      }
-      if constexpr (F::kKMin) split_pair(qs0, qs1, qsb_hi, qsb_lo);
-      const float cr = __uint_as_float(static_cast<uint32_t>(ex) << 23) * (1.0f / 16.0f) * 1.4426950408889634f;
+      });
       crow[0] = __shfl_sync(0xffffffffu, cr, (2 * t) * 4);
       crow[1] = __shfl_sync(0xffffffffu, cr, (2 * t + 1) * 4);
     }
@@ -480,25 +542,18 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_b
     // positions of the thread's two rows (rows past the last take the last's: never stored)
     int qpos[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) qpos[c] = un.pos0 + min((nt0 * 8 + 2 * t + c) / p.group, un.rows - 1);
+    for (int c = 0; c < 2; ++c) qpos[c] = un.pos0 + min((2 * t + c) / p.group, un.rows - 1);
     const int last = un.pos0 + un.rows - 1;
     const int span = p.window > 0 ? p.window : INT_MAX;
     for (; k < end; ++k) {
       const int st = k % C::kStages;
-      // this warp's copies of tile k are done, and with the barrier everybody's are seen
-      if constexpr (NT == 1) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
-        __syncwarp();
-      } else {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-        asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "n"(NT * 32) : "memory");
-        issue(k + C::kStages - 1);  // into the stage of tile k - 1, which the group is done with
-      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+      __syncwarp();
       const int key = *reinterpret_cast<volatile int*>(&key_of[st]);
       if (key >= 0) {
-        const uint32_t kb = ring + st * C::kTileBytes;
+        const uint32_t kb = ring_s + st * C::kTileBytes;
         if (key + 15 > last) {
-          uint8_t* vs = smem + (kb - smem_u32(smem)) + L::kV + L::kVScale;
+          uint8_t* vs = ring + st * C::kTileBytes + L::kV + L::kVScale;
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
@@ -510,13 +565,11 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_b
             },
             m_run, l_run, oacc, racc);
       }
-      if constexpr (NT == 1) {
-        __syncwarp();
-        issue(k + C::kStages);
-      }
+      __syncwarp();
+      issue(k + C::kStages);
     }
 
-    // ---- the rows: 2t, 2t + 1 of the n-tile, dims 16 i + g, + 8
+    // ---- rows 2t, 2t + 1, dims 16 i + g, + 8
     if constexpr (F::kVMin) {
       // zero-point values: the minimum terms of block b for rows 2t, 2t + 1 sit in lane 4b + t
 #pragma unroll
@@ -548,7 +601,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_b
       // a row that saw no key: l = 0 (a NaN stays one)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float lse2 = l == 0.f ? -INFINITY : m_run[c] + log2f(l);
-      const int row = nt0 * 8 + 2 * t + c;
+      const int row = 2 * t + c;
       if (row >= n_rows) continue;
       if (whole) {
         const int qi = row / p.group, hq = w.h * p.group + row - qi * p.group;
@@ -571,7 +624,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_b
         if (g == 0) p.part_lse[at] = lse2;
       }
     }
-    if (nt0 == 0 && lane == 0) {
+    if (lane == 0) {
       int2* parts = p.unit_parts + w.unit;
       if (start >= 0) parts->x = slot;
       if (start + w.n <= n_tiles) parts->y = slot >> 1;
@@ -582,6 +635,386 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, NT, T>::kThreads, 1) decode_b
     __syncwarp();  // every lane has read the unit and its fragments
     if (lane == 0) *mine = nx;
     __syncwarp();
+  }
+}
+
+// ---- 9 to 24 query rows: four warps per group.  A step is up to four tiles of a unit.  Warp w takes
+// the scores of tile w for all NR n-tiles of rows; the four agree on the rows' running maxima (a
+// barrier that also votes: mostly none moves); each puts its P into shared memory as B fragments;
+// behind a second barrier warp w adds channels 64 w .. + 63 of all four tiles' values.
+template <int KF, int VF, int NR, typename T>
+__global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
+    decode_batch_wide_kernel(const BatchDecodeParams p) {
+  using C = WideCfg<KF, VF, NR, T>;
+  using F = TileFormat<KF, VF>;
+  using L = SingleTileLayout<KF, VF>;
+  constexpr int QP = BatchParts<T>::kQ, PP = BatchParts<T>::kP;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int grp = warp >> 2, w = warp & 3;
+  auto* plan = reinterpret_cast<BatchPlanState<C::kWarps, C::kGroups>*>(smem + C::kMetaOff);
+  // [kStages][4]: first position of each tile of the group's steps, -1: none
+  int* key_of = reinterpret_cast<int*>(plan + 1) + grp * 4 * C::kStages;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // only now, so that the merge grid may read the batch's arrays before this grid is done
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!plan_stretches<C>(p, plan)) return;
+  const int n_tiles = plan->to[grp] - plan->from[grp];
+  if (n_tiles <= 0) return;  // the whole group
+
+  uint8_t* ring = smem + grp * C::kGroupBytes;
+  const uint32_t ring_s = smem_u32(ring), q_s = ring_s + C::kStages * C::kStepBytes;
+  const uint32_t p_s = q_s + NR * C::kQTileBytes;
+  auto* state = reinterpret_cast<WideState<NR>*>(ring + C::kStages * C::kStepBytes + NR * C::kQTileBytes + 4 * C::kPTileBytes);
+  Producer* prod = &plan->producer[warp];
+  auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory"); };
+
+  int2 ahead = make_int2(-2, 0);  // this warp's entry of the next step to be copied, loaded a step ahead
+  // starts the copies of this warp's tile of the next step into stage st, and moves on
+  auto issue = [&](int st) {
+    const int k0 = lds_int(&prod->next);
+    if (k0 < n_tiles) {
+      const int u = lds_int(&prod->unit), start = lds_int(&prod->start);
+      const int end = min(start + lds_int(&prod->n), n_tiles);
+      int key = -1;
+      if (k0 + w < end) {
+        const int last = lds_int(&prod->last), low = lds_int(&prod->low);
+        const int G = (lds_int(&prod->t0) + k0 + w - start) & 7;
+        if (fetch_block(p, ahead, last, low, lane)) {
+          key = ahead.y * kPageTokens + 16 * G;
+          if (key > last || key + 15 < low) key = -1;
+        }
+        if (key >= 0)
+          copy_tile<KF, VF>(ring_s + st * C::kStepBytes + w * C::kTileBytes, p.b.k_pool + ahead.x * p.b.k_stride,
+                            p.b.v_pool + ahead.x * p.b.v_stride, G, lane);
+      }
+      __syncwarp();
+      if (lane == 0) *reinterpret_cast<volatile int*>(&key_of[4 * st + w]) = key;
+      // the step after it: of this unit, or the first of the next
+      int next = k0 + 4, unit = u, unit_start = start, unit_end = end;
+      int t0 = lds_int(&prod->t0);
+      if (next >= end) {
+        next = end;
+        if (end < n_tiles) {
+          const BatchUnit nx = next_unit(p, u);
+          producer_unit(p, prod, nx, end, lane);
+          unit = nx.unit;
+          unit_start = end;
+          unit_end = min(end + nx.n, n_tiles);
+          t0 = nx.t0;
+        }
+      }
+      if (lane == 0) prod->next = next;
+      __syncwarp();
+      if (next < n_tiles && next + w < unit_end) ahead = page_of(p, unit, (t0 + next + w - unit_start) >> 3);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  BatchUnit* mine = &plan->at_work[warp];
+  int start = -plan->skip[grp];  // first tile of the unit, in the group's numbering
+  int k = 0;                     // tiles this group has consumed
+  int step = 0;
+  if (lane == 0) {
+    *mine = plan->unit[grp];
+    prod->next = 0;
+  }
+  __syncwarp();
+  producer_unit(p, prod, *mine, start, lane);
+
+  while (true) {
+    const BatchUnit un = *mine;
+    const int end = min(start + un.n, n_tiles);  // the group's tiles of the unit: [k, end)
+
+    // ---- the query's fragments: warp n those of n-tile n
+    {
+      if (k == 0 && w < end) ahead = page_of(p, un.unit, (un.t0 + w - start) >> 3);
+      auto fill = [&]() {
+        if (k == 0)
+          for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+      };
+      if (w < NR) {
+        uint32_t qsb_hi = 0u, qsb_lo = 0u;
+        const float cr =
+            query_fragments<T, QP, F::kKMin>(p, un, w, lane, q_s + w * C::kQTileBytes, qsb_hi, qsb_lo, fill);
+        if (t == 0) state->crow[8 * w + g] = cr;
+        if constexpr (F::kKMin) state->qsums[w][lane] = make_uint2(qsb_hi, qsb_lo);
+      } else {
+        fill();
+        // positions of the rows (rows past the last take the last's: never stored)
+        if (w == 3 && lane < 8 * NR) state->qpos[lane] = un.pos0 + min(lane / p.group, un.rows - 1);
+      }
+    }
+    group_sync();
+    float crow[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) crow[n][c] = state->crow[8 * n + 2 * t + c];
+
+    float m_run[NR][2], l_run[NR][2];
+    float oacc[4][NR][4], racc[NR][4];  // dims 64 w + 16 i + g (+ 8); zero-point values: all blocks' minimum terms
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) m_run[n][c] = -INFINITY, l_run[n][c] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        racc[n][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) oacc[i][n][e] = 0.f;
+      }
+    }
+    const int last = un.pos0 + un.rows - 1, pos0 = un.pos0;
+    const int span = p.window > 0 ? p.window : INT_MAX;
+
+    for (; k < end; k += 4, ++step) {
+      const int st = step % C::kStages;
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+      __syncwarp();
+      const int key = *reinterpret_cast<volatile int*>(&key_of[4 * st + w]);
+      const uint32_t kb = ring_s + st * C::kStepBytes + w * C::kTileBytes;
+      const bool live = k + w < end && key >= 0;
+      float sv[NR][4];
+      if (live) {
+        if (key + 15 > last) {
+          uint8_t* vs = ring + st * C::kStepBytes + w * C::kTileBytes + L::kV + L::kVScale;
+          blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
+        }
+        tile_scores<L, KF, VF, QP, NR>(
+            kb, 0, g, t,
+            [&](int n, int bl, int ks) -> uint4 {
+              const uint32_t from = q_s + n * C::kQTileBytes + ((bl * 2 + ks) * 32 + lane) * C::kQFragBytes;
+              if constexpr (QP == 2) {
+                return lds128(from);
+              } else {
+                uint2 v;
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from));
+                return make_uint4(v.x, v.y, 0u, 0u);
+              }
+            },
+            [&](int n) { return state->qsums[n][lane]; }, sv);
+        const bool need_mask = key + 15 > pos0 || key <= last - span;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[n][e] *= crow[n][e & 1];
+        if (need_mask) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = key + g + 8 * (e >> 1), qpos = state->qpos[8 * n + 2 * t + (e & 1)];
+              if (at > qpos || at <= qpos - span) sv[n][e] = -INFINITY;
+            }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[n][e] = -INFINITY;
+      }
+      // ---- the running maxima (within 2^2 of the rows' own, as in the one-warp kernel)
+      uint32_t need = 0;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) need |= fmaxf(sv[n][c], sv[n][c + 2]) > m_run[n][c] + 2.f;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.u32 q, %1, 0;\n\t"
+          "bar.red.or.pred p, %2, 128, q;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(need)
+          : "r"(need), "r"(grp + 1)
+          : "memory");
+      // every warp is done with the step before this one: its stage takes the step S - 1 ahead
+      issue((step + C::kStages - 1) % C::kStages);
+      if (need) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(sv[n][c], sv[n][c + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (g == 0) state->top[w][8 * n + 2 * t + c] = mx;
+          }
+        group_sync();
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int row = 8 * n + 2 * t + c;
+            const float mx = fmaxf(fmaxf(state->top[0][row], state->top[1][row]),
+                                   fmaxf(state->top[2][row], state->top[3][row]));
+            if (mx > m_run[n][c] + 2.f) {
+              const float alpha = fast_exp2(m_run[n][c] - mx);  // 0 when m_run = -inf
+              l_run[n][c] *= alpha;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                oacc[i][n][c] *= alpha;
+                oacc[i][n][c + 2] *= alpha;
+              }
+              if constexpr (F::kVMin) racc[n][c] *= alpha;
+              m_run[n][c] = mx;
+            }
+          }
+      }
+      // ---- P, as B fragments
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        float pr[4];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float mu = m_run[n][c] == -INFINITY ? 0.f : m_run[n][c];
+          pr[c] = fast_exp2(sv[n][c] - mu);
+          pr[c + 2] = fast_exp2(sv[n][c + 2] - mu);
+          l_run[n][c] += pr[c] + pr[c + 2];
+        }
+        const uint32_t to = p_s + w * C::kPTileBytes + (n * 32 + lane) * C::kPFragBytes;
+        if constexpr (PP == 2) {
+          uint32_t h01, l01, h23, l23;
+          split_pair(pr[0], pr[1], h01, l01);
+          split_pair(pr[2], pr[3], h23, l23);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(movmatrix_t(h01)),
+                       "r"(movmatrix_t(h23)), "r"(movmatrix_t(l01)), "r"(movmatrix_t(l23))
+                       : "memory");
+        } else {
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(movmatrix_t(pack_half2(pr[0], pr[1]))),
+                       "r"(movmatrix_t(pack_half2(pr[2], pr[3])))
+                       : "memory");
+        }
+      }
+      group_sync();
+      // ---- O^T += V^T P^T for this warp's channels, over the step's tiles
+#pragma unroll 1
+      for (int u = 0; u < 4 && k + u < end; ++u) {
+        if (*reinterpret_cast<volatile int*>(&key_of[4 * st + u]) < 0) continue;  // nothing was fetched
+        const uint32_t vb = ring_s + st * C::kStepBytes + u * C::kTileBytes + L::kV;
+        uint32_t ph[NR][2], pl[NR][2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          const uint32_t from = p_s + u * C::kPTileBytes + (n * 32 + lane) * C::kPFragBytes;
+          if constexpr (PP == 2) {
+            const uint4 v = lds128(from);
+            ph[n][0] = v.x, ph[n][1] = v.y, pl[n][0] = v.z, pl[n][1] = v.w;
+          } else {
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(ph[n][0]), "=r"(ph[n][1]) : "r"(from));
+            pl[n][0] = pl[n][1] = 0u;
+          }
+        }
+        int e = 0;  // constant in the unrolled code
+        tile_value_pair<L, KF, VF>(
+            vb, 0, w, g, t, [&](int, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
+#pragma unroll
+              for (int n = 0; n < NR; ++n) {
+                uint32_t bh0, bl0, bh1, bl1;
+                scale_p<PP>(ph[n][0], pl[n][0], d0, bh0, bl0);
+                scale_p<PP>(ph[n][1], pl[n][1], d1, bh1, bl1);
+                mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
+                if constexpr (PP == 2) mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
+                mma_f16(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
+                if constexpr (PP == 2) mma_f16(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
+              }
+              ++e;
+            });
+        if constexpr (F::kVMin) {
+          uint32_t m01, m89;
+          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                       : "=r"(m01), "=r"(m89)
+                       : "r"(vb + L::kVMinimum + ((t * 8 + g) * 4) * 2));
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            mma_f16(racc[n], m01, 0u, m89, 0u, ph[n][0], ph[n][1]);
+            if constexpr (PP == 2) mma_f16(racc[n], m01, 0u, m89, 0u, pl[n][0], pl[n][1]);
+          }
+        }
+      }
+    }
+    k = end;
+
+    // ---- rows 8n + 2t (+ 1), dims 64 w + 16 i + g (+ 8)
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float l = l_run[n][c];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) state->sum[w][8 * n + 2 * t + c] = l;
+      }
+    if constexpr (F::kVMin) {
+      // the minimum terms of block b for rows 2t, 2t + 1 sit in lane 4b + t
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float v = __shfl_sync(0xffffffffu, racc[n][c], 4 * (2 * w + e) + t);
+#pragma unroll
+            for (int i = 2 * e; i < 2 * e + 2; ++i) {
+              oacc[i][n][c] += v;
+              oacc[i][n][c + 2] += v;
+            }
+          }
+    }
+    group_sync();
+    BatchUnit wk;  // the unit again
+    wk.unit = lds_int(&mine->unit);
+    wk.h = lds_int(&mine->h);
+    wk.r0 = lds_int(&mine->r0);
+    wk.n = lds_int(&mine->n);
+    const int n_rows = lds_int(&mine->rows) * p.group;
+    const bool whole = start >= 0 && start + wk.n <= n_tiles;
+    const int slot = (grp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)) * 2 + (start <= 0 ? 0 : 1);
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = 8 * n + 2 * t + c;
+        if (row >= n_rows) continue;
+        const float l = (state->sum[0][row] + state->sum[1][row]) + (state->sum[2][row] + state->sum[3][row]);
+        // a row that saw no key: l = 0 (a NaN stays one)
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float lse2 = l == 0.f ? -INFINITY : m_run[n][c] + log2f(l);
+        if (whole) {
+          const int qi = row / p.group, hq = wk.h * p.group + row - qi * p.group;
+          T* to = static_cast<T*>(p.out.data) + (wk.r0 + qi) * p.out.row_stride + hq * p.out.head_stride + 64 * w + g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            to[16 * i] = static_cast<T>(oacc[i][n][c] * inv);
+            to[16 * i + 8] = static_cast<T>(oacc[i][n][c + 2] * inv);
+          }
+          if (w == 0 && g == 0)
+            p.lse[static_cast<long long>(wk.r0 + qi) * (p.b.n_kv * p.group) + hq] = lse2 * 0.69314718055994531f;
+        } else {
+          const long long at = static_cast<long long>(slot) * C::kRowsPad + row;
+          float* to = p.part_o + at * kHeadDim + 64 * w + g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            to[16 * i] = oacc[i][n][c] * inv;
+            to[16 * i + 8] = oacc[i][n][c + 2] * inv;
+          }
+          if (w == 0 && g == 0) p.part_lse[at] = lse2;
+        }
+      }
+    if (w == 0 && lane == 0) {
+      int2* parts = p.unit_parts + wk.unit;
+      if (start >= 0) parts->x = slot;
+      if (start + wk.n <= n_tiles) parts->y = slot >> 1;
+    }
+    if (k == n_tiles) break;
+    start = k;
+    const BatchUnit nx = next_unit(p, wk.unit);
+    __syncwarp();
+    if (lane == 0) *mine = nx;
+    group_sync();  // the sums and the fragments, before the next unit's
   }
 }
 
@@ -673,24 +1106,25 @@ __global__ void __launch_bounds__(256) merge_batch_kernel(const BatchDecodeParam
 int batch_row_tiles(int rows) { return (rows + 7) / 8; }
 
 // Groups that the split grid can have: the workspace is sized by it.
-int batch_group_bound(int sms, int n_tiles8) { return sms * (12 / n_tiles8); }
+int batch_group_bound(int sms, int n_tiles8) { return sms * (n_tiles8 == 1 ? 12 : 3); }
 
-template <int KF, int VF, int NT, typename T>
-static cudaError_t launch_batch_t(const BatchDecodeParams& p, int sms, long long most_tiles, cudaStream_t stream) {
-  using C = BatchCfg<KF, VF, NT, T>;
+template <typename C, typename T>
+static cudaError_t launch_batch_t(void (*kernel)(BatchDecodeParams), const BatchDecodeParams& p, int sms,
+                                  long long most_tiles, cudaStream_t stream) {
   const long long units = static_cast<long long>(p.b.n_seqs) * p.b.n_kv;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const long long groups = (most_tiles + C::kUnitCost * units) / C::kMinShare + 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(sms, (groups + C::kGroups - 1) / C::kGroups)));
+  // every stretch is kMinShare long at least, and the first ones go to different SMs
+  const long long stretches = (most_tiles + C::kUnitCost * units) / C::kMinShare + 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(sms, stretches)));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_batch_kernel<KF, VF, NT, T>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(units), units <= 296 ? std::min(p.group * p.b.max_rows, 24) : 1);
   cfg.blockDim = dim3(256);
@@ -705,9 +1139,11 @@ static cudaError_t launch_batch_t(const BatchDecodeParams& p, int sms, long long
 template <int KF, int VF, typename T>
 static cudaError_t launch_batch_rows(const BatchDecodeParams& p, int sms, long long most_tiles, cudaStream_t stream) {
   switch (batch_row_tiles(p.group * p.b.max_rows)) {
-    case 1: return launch_batch_t<KF, VF, 1, T>(p, sms, most_tiles, stream);
-    case 2: return launch_batch_t<KF, VF, 2, T>(p, sms, most_tiles, stream);
-    default: return launch_batch_t<KF, VF, 3, T>(p, sms, most_tiles, stream);
+    case 1: return launch_batch_t<BatchCfg<KF, VF, T>, T>(decode_batch_kernel<KF, VF, T>, p, sms, most_tiles, stream);
+    case 2:
+      return launch_batch_t<WideCfg<KF, VF, 2, T>, T>(decode_batch_wide_kernel<KF, VF, 2, T>, p, sms, most_tiles, stream);
+    default:
+      return launch_batch_t<WideCfg<KF, VF, 3, T>, T>(decode_batch_wide_kernel<KF, VF, 3, T>, p, sms, most_tiles, stream);
   }
 }
 
@@ -723,21 +1159,26 @@ cudaError_t launch_decode_batch(const BatchDecodeParams& p, int dtype, int k_fmt
   return cudaErrorInvalidValue;
 }
 
-template <int KF, int VF, int NT, typename T>
+template <int KF, int VF, typename T>
 static cudaError_t prepare_batch_t() {
-  return cudaFuncSetAttribute(decode_batch_kernel<KF, VF, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              BatchCfg<KF, VF, NT, T>::kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(decode_batch_kernel<KF, VF, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       BatchCfg<KF, VF, T>::kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(decode_batch_wide_kernel<KF, VF, 2, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WideCfg<KF, VF, 2, T>::kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(decode_batch_wide_kernel<KF, VF, 3, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WideCfg<KF, VF, 3, T>::kSmemBytes);
+  return e;
 }
 
 cudaError_t prepare_batch_kernels() {
   cudaError_t e;
-#define KV_SET1(KF, VF, NT, T) \
-  if ((e = prepare_batch_t<KF, VF, NT, T>()) != cudaSuccess) return e;
-#define KV_SET2(KF, VF, T) KV_SET1(KF, VF, 1, T) KV_SET1(KF, VF, 2, T) KV_SET1(KF, VF, 3, T)
-#define KV_SET(KF, VF) KV_SET2(KF, VF, float) KV_SET2(KF, VF, __half) KV_SET2(KF, VF, __nv_bfloat16)
+#define KV_SET1(KF, VF, T) \
+  if ((e = prepare_batch_t<KF, VF, T>()) != cudaSuccess) return e;
+#define KV_SET(KF, VF) KV_SET1(KF, VF, float) KV_SET1(KF, VF, __half) KV_SET1(KF, VF, __nv_bfloat16)
   KVATTN_BATCH_PAIRS(KV_SET)
 #undef KV_SET
-#undef KV_SET2
 #undef KV_SET1
   return cudaSuccess;
 }

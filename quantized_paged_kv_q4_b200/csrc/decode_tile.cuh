@@ -100,27 +100,25 @@ struct SingleTileLayout {
   static constexpr int kBytes = kSmall + 256 * kNarrow;
 };
 
-// Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
-// lane % 4; the thread's rows are 2t, 2t + 1).
-//   QP, PP       f16 parts of the query and of P: 2 keeps about 22 bits of each, 1 rounds once
-//   qfrag(b, ks) the query's B fragments of block b, k-step ks (hi0, hi1, lo0, lo1)
-//   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment
-//   crow         turns a dot product with the normalised row into a base-2 softmax score
-//   grow         how far, in powers of two, a score may pass the running maximum (p <= 2^grow)
-//   mask(e, x)   x, or -inf where the key is unseen: token g + 8 (e / 2), row 2t + e % 2
-// The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
-template <typename L, int KF, int VF, int QP, int PP, typename QFrag, typename Mask>
-__device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
-                                            uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], float grow,
-                                            Mask mask, float (&m_run)[2], float (&l_run)[2],
-                                            float (&oacc)[2 * kTileBlocks][4], float (&racc)[4]) {
+// S = K Q^T of one tile of 16 tokens and NR n-tiles of 8 query rows (one warp; g = lane / 4, t = lane %
+// 4): sacc[n][e] is token g + 8 (e / 2), row 2t + e % 2 of n-tile n.
+//   QP             f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
+//   qfrag(n, b, ks) the B fragments of n-tile n, block b, k-step ks (hi0, hi1, lo0, lo1)
+//   qsums(n)       zero-point keys: the query's block sums as a B fragment (hi, lo)
+// The tile is tile G of the copy at kb, arranged as L.
+template <typename L, int KF, int VF, int QP, int NR, typename QFrag, typename QSums>
+__device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QFrag qfrag, QSums qsums,
+                                            float (&sacc)[NR][4]) {
   using F = TileFormat<KF, VF>;
   // ---------------- S = K Q^T over the 256 channels ----------------
   // Key codes enter the MMA exactly (integers in f16).  Each 32-channel block is
   // accumulated on its own (two k-steps, each with the query's parts) and then
   // scaled by the block's fp32 scale into S; with a zero point, two more MMAs add the
   // block minima times the query block sums.
-  float sacc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sacc[n][e] = 0.f;
   // key scales of rows g (H=0) and g+8 (H=1) for the 8 blocks, fp32; zero-point keys:
   // the minima of blocks 2t, 2t + 1 of the same rows (the A fragment of the MMA that
   // adds the minimum terms)
@@ -141,14 +139,17 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
   }
   // one block: an MMA per k-step and query part into xb, then S += d * xb
   auto block_qk = [&](int bl, const uint32_t (&A)[2][4]) {
-    float xb[4];
-    const uint4 f0 = qfrag(bl, 0), f1 = qfrag(bl, 1);
-    mma_f16_z(xb, A[0][0], A[0][1], A[0][2], A[0][3], f0.x, f0.y);
-    if constexpr (QP == 2) mma_f16(xb, A[0][0], A[0][1], A[0][2], A[0][3], f0.z, f0.w);
-    mma_f16(xb, A[1][0], A[1][1], A[1][2], A[1][3], f1.x, f1.y);
-    if constexpr (QP == 2) mma_f16(xb, A[1][0], A[1][1], A[1][2], A[1][3], f1.z, f1.w);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sacc[e] = fmaf(dkf[e >> 1][bl], xb[e], sacc[e]);
+    for (int n = 0; n < NR; ++n) {
+      float xb[4];
+      const uint4 f0 = qfrag(n, bl, 0), f1 = qfrag(n, bl, 1);
+      mma_f16_z(xb, A[0][0], A[0][1], A[0][2], A[0][3], f0.x, f0.y);
+      if constexpr (QP == 2) mma_f16(xb, A[0][0], A[0][1], A[0][2], A[0][3], f0.z, f0.w);
+      mma_f16(xb, A[1][0], A[1][1], A[1][2], A[1][3], f1.x, f1.y);
+      if constexpr (QP == 2) mma_f16(xb, A[1][0], A[1][1], A[1][2], A[1][3], f1.z, f1.w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sacc[n][e] = fmaf(dkf[e >> 1][bl], xb[e], sacc[n][e]);
+    }
   };
   if constexpr (KF == kKeyQ8) {
 #pragma unroll
@@ -227,9 +228,81 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
     // S += sum_b m[token][b] qsum[b][row] as one MMA per part of the block sums: A =
     // the minima (tokens g, g + 8 x blocks 2t, 2t + 1; k = 8..15 is zero, exact in f16),
     // B = the block sums of the query rows; the products accumulate in fp32
-    mma_f16(sacc, mka[0], mka[1], 0u, 0u, qsb_hi, 0u);
-    mma_f16(sacc, mka[0], mka[1], 0u, 0u, qsb_lo, 0u);
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const uint2 qs = qsums(n);
+      mma_f16(sacc[n], mka[0], mka[1], 0u, 0u, qs.x, 0u);
+      mma_f16(sacc[n], mka[0], mka[1], 0u, 0u, qs.y, 0u);
+    }
   }
+}
+
+// The codes of value blocks 2C and 2C + 1 of one tile as A fragments (16 dims x 16 tokens, exact in f16):
+// f(block, dims 0-15, dims 16-31, scales of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9).
+template <typename L, int KF, int VF, typename Use>
+__device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g, int t, Use f) {
+  using F = TileFormat<KF, VF>;
+  if constexpr (VF != kValQ8) {
+    const uint4 vw = lds128(vb + ((((G * 4 + C) * 8 + g) * 4 + t) * 16));
+    const uint32_t sidx = vb + L::kVScale + (((G * 4 + t) * 8 + 2 * C) * 4) * 2;
+    const uint4 dv = lds128(sidx);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t W0 = e ? vw.z : vw.x, W1 = e ? vw.w : vw.y;
+      const uint32_t W0s = W0 >> 8, W1s = W1 >> 8;
+      // Q4_0: q - 8 (1024 + q - 1032, or (1024 + 16q) / 16 - 72); Q4_1: q
+      constexpr uint32_t kSubLo = F::kVMin ? kHalf2Magic : kHalf2_1032;
+      constexpr uint32_t kAddHi = F::kVMin ? kHalf2_m64 : kHalf2_m72;
+      const uint32_t a0[4] = {hsub2(and_or(W0, 0x000F000Fu, kHalf2Magic), kSubLo),
+                              hfma2(and_or(W0, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi),
+                              hsub2(and_or(W1, 0x000F000Fu, kHalf2Magic), kSubLo),
+                              hfma2(and_or(W1, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi)};
+      const uint32_t a1[4] = {hsub2(and_or(W0s, 0x000F000Fu, kHalf2Magic), kSubLo),
+                              hfma2(and_or(W0s, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi),
+                              hsub2(and_or(W1s, 0x000F000Fu, kHalf2Magic), kSubLo),
+                              hfma2(and_or(W1s, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi)};
+      f(2 * C + e, a0, a1, e ? dv.z : dv.x, e ? dv.w : dv.y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int b = 2 * C + e;
+      const uint4 vw = lds128(vb + ((((G * 8 + b) * 8 + g) * 4 + t) * 16));
+      uint32_t d0, d1;
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                   : "=r"(d0), "=r"(d1)
+                   : "r"(vb + L::kVScale + (((G * 4 + t) * 8 + b) * 4) * 2));
+      const uint32_t w[4] = {vw.x, vw.y, vw.z, vw.w};  // offset-binary code bytes (q + 128)
+      uint32_t a[2][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        a[q >> 1][2 * (q & 1)] = hsub2(prmt(w[q], kByte64x4, 0x4140u), kHalf2_1152);
+        a[q >> 1][2 * (q & 1) + 1] = hsub2(prmt(w[q], kByte64x4, 0x4342u), kHalf2_1152);
+      }
+      f(b, a[0], a[1], d0, d1);
+    }
+  }
+}
+
+// Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
+// lane % 4; the thread's rows are 2t, 2t + 1).
+//   QP, PP       f16 parts of the query and of P: 2 keeps about 22 bits of each, 1 rounds once
+//   qfrag(b, ks) the query's B fragments of block b, k-step ks (hi0, hi1, lo0, lo1)
+//   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment
+//   crow         turns a dot product with the normalised row into a base-2 softmax score
+//   grow         how far, in powers of two, a score may pass the running maximum (p <= 2^grow)
+//   mask(e, x)   x, or -inf where the key is unseen: token g + 8 (e / 2), row 2t + e % 2
+// The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
+template <typename L, int KF, int VF, int QP, int PP, typename QFrag, typename Mask>
+__device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
+                                            uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], float grow,
+                                            Mask mask, float (&m_run)[2], float (&l_run)[2],
+                                            float (&oacc)[2 * kTileBlocks][4], float (&racc)[4]) {
+  using F = TileFormat<KF, VF>;
+  float sacc[1][4];
+  tile_scores<L, KF, VF, QP, 1>(
+      kb, G, g, t, [&](int, int bl, int ks) { return qfrag(bl, ks); }, [&](int) { return make_uint2(qsb_hi, qsb_lo); },
+      sacc);
   // ---------------- online softmax (base 2) ----------------
   // The running maximum m_run of a row is shared by the 8 lanes that hold the row.
   // It only has to bound the scores to within 2^grow (p <= 2^grow in f16), so the exact
@@ -239,7 +312,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
   bool need = false;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    sv[e] = mask(e, sacc[e] * crow[e & 1]);
+    sv[e] = mask(e, sacc[0][e] * crow[e & 1]);
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -293,72 +366,28 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
   // ---------------- O^T += V^T P^T ----------------
   // V codes enter the MMA exactly; the per-token block scale multiplies P (in PP f16
   // parts), PP MMAs per 16-dimension half.
-  if constexpr (VF != kValQ8) {
 #pragma unroll
-    for (int Cc = 0; Cc < kTileBlocks / 2; ++Cc) {
-      const uint4 vw = lds128(vb + ((((G * 4 + Cc) * 8 + g) * 4 + t) * 16));
-      const uint32_t sidx = vb + L::kVScale + (((G * 4 + t) * 8 + 2 * Cc) * 4) * 2;
-      const uint4 dv = lds128(sidx);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int bl = 2 * Cc + e;
-        const uint32_t W0 = e ? vw.z : vw.x, W1 = e ? vw.w : vw.y;
-        const uint32_t d0 = e ? dv.z : dv.x, d1 = e ? dv.w : dv.y;
-        const uint32_t W0s = W0 >> 8, W1s = W1 >> 8;
-        // Q4_0: q - 8 (1024 + q - 1032, or (1024 + 16q) / 16 - 72); Q4_1: q
-        constexpr uint32_t kSubLo = F::kVMin ? kHalf2Magic : kHalf2_1032;
-        constexpr uint32_t kAddHi = F::kVMin ? kHalf2_m64 : kHalf2_m72;
-        const uint32_t a00 = hsub2(and_or(W0, 0x000F000Fu, kHalf2Magic), kSubLo);
-        const uint32_t a01 = hfma2(and_or(W0, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi);
-        const uint32_t a02 = hsub2(and_or(W1, 0x000F000Fu, kHalf2Magic), kSubLo);
-        const uint32_t a03 = hfma2(and_or(W1, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi);
-        const uint32_t a10 = hsub2(and_or(W0s, 0x000F000Fu, kHalf2Magic), kSubLo);
-        const uint32_t a11 = hfma2(and_or(W0s, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi);
-        const uint32_t a12 = hsub2(and_or(W1s, 0x000F000Fu, kHalf2Magic), kSubLo);
-        const uint32_t a13 = hfma2(and_or(W1s, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kAddHi);
-        uint32_t bh0, bl0, bh1, bl1;
-        scale_p<PP>(pbh[0], pbl[0], d0, bh0, bl0);
-        scale_p<PP>(pbh[1], pbl[1], d1, bh1, bl1);
-        mma_f16(oacc[2 * bl], a00, a01, a02, a03, bh0, bh1);
-        if constexpr (PP == 2) mma_f16(oacc[2 * bl], a00, a01, a02, a03, bl0, bl1);
-        mma_f16(oacc[2 * bl + 1], a10, a11, a12, a13, bh0, bh1);
-        if constexpr (PP == 2) mma_f16(oacc[2 * bl + 1], a10, a11, a12, a13, bl0, bl1);
-      }
-    }
-    if constexpr (F::kVMin) {
-      // sum over the tile's tokens of p * m for all 8 blocks at once: A = the minima
-      // (block g x tokens 2t, 2t + 1 | 2t + 8, 2t + 9, exact in f16; blocks 8..15 zero),
-      // B = P^T as its high and low parts
-      uint32_t m01, m89;
-      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                   : "=r"(m01), "=r"(m89)
-                   : "r"(vb + L::kVMinimum + (((G * 4 + t) * 8 + g) * 4) * 2));
-      mma_f16(racc, m01, 0u, m89, 0u, pbh[0], pbh[1]);
-      if constexpr (PP == 2) mma_f16(racc, m01, 0u, m89, 0u, pbl[0], pbl[1]);
-    }
-  } else {
-#pragma unroll
-    for (int b = 0; b < kTileBlocks; ++b) {
-      const uint4 vw = lds128(vb + ((((G * 8 + b) * 8 + g) * 4 + t) * 16));
-      uint32_t d0, d1;
-      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                   : "=r"(d0), "=r"(d1)
-                   : "r"(vb + L::kVScale + (((G * 4 + t) * 8 + b) * 4) * 2));
-      const uint32_t w[4] = {vw.x, vw.y, vw.z, vw.w};  // offset-binary code bytes (q + 128)
-      uint32_t a[4][2];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        a[q][0] = hsub2(prmt(w[q], kByte64x4, 0x4140u), kHalf2_1152);
-        a[q][1] = hsub2(prmt(w[q], kByte64x4, 0x4342u), kHalf2_1152);
-      }
+  for (int C = 0; C < kTileBlocks / 2; ++C)
+    tile_value_pair<L, KF, VF>(vb, G, C, g, t,
+                               [&](int bl, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
       uint32_t bh0, bl0, bh1, bl1;
       scale_p<PP>(pbh[0], pbl[0], d0, bh0, bl0);
       scale_p<PP>(pbh[1], pbl[1], d1, bh1, bl1);
-      mma_f16(oacc[2 * b], a[0][0], a[0][1], a[1][0], a[1][1], bh0, bh1);
-      if constexpr (PP == 2) mma_f16(oacc[2 * b], a[0][0], a[0][1], a[1][0], a[1][1], bl0, bl1);
-      mma_f16(oacc[2 * b + 1], a[2][0], a[2][1], a[3][0], a[3][1], bh0, bh1);
-      if constexpr (PP == 2) mma_f16(oacc[2 * b + 1], a[2][0], a[2][1], a[3][0], a[3][1], bl0, bl1);
-    }
+      mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
+      if constexpr (PP == 2) mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
+      mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
+      if constexpr (PP == 2) mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
+    });
+  if constexpr (F::kVMin) {
+    // sum over the tile's tokens of p * m for all 8 blocks at once: A = the minima
+    // (block g x tokens 2t, 2t + 1 | 2t + 8, 2t + 9, exact in f16; blocks 8..15 zero),
+    // B = P^T as its high and low parts
+    uint32_t m01, m89;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(m01), "=r"(m89)
+                 : "r"(vb + L::kVMinimum + (((G * 4 + t) * 8 + g) * 4) * 2));
+    mma_f16(racc, m01, 0u, m89, 0u, pbh[0], pbh[1]);
+    if constexpr (PP == 2) mma_f16(racc, m01, 0u, m89, 0u, pbl[0], pbl[1]);
   }
 }
 
