@@ -109,6 +109,7 @@ struct BatchCfg {
   static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
   // What a unit costs beside its tiles, and the least a group takes, in tiles.
   static constexpr int kUnitCost = 2, kMinShare = 4;
+  static constexpr int kPair = 2;
 };
 
 // The wide kernel's state of a unit, per group: rows in order.
@@ -142,6 +143,7 @@ struct WideCfg {
   static_assert(kGroups >= 1 && kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
   static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
   static constexpr int kUnitCost = 6, kMinShare = 8;
+  static constexpr int kPair = 2;
 };
 
 __device__ __forceinline__ int lds_int(const int* p) { return static_cast<int>(lds32(smem_u32(p))); }
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
-        attend_tile<L, KF, VF, QP, PP>(
+        attend_tile<L, KF, VF, QP, PP, C::kPair>(
             kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow, 2.f,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
@@ -783,7 +785,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           uint8_t* vs = ring + st * C::kStepBytes + w * C::kTileBytes + L::kV + L::kVScale;
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
-        tile_scores<L, KF, VF, QP, NR>(
+        tile_scores<L, KF, VF, QP, NR, C::kPair>(
             kb, 0, g, t,
             [&](int n, int bl, int ks) -> uint4 {
               const uint32_t from = q_s + n * C::kQTileBytes + ((bl * 2 + ks) * 32 + lane) * C::kQFragBytes;
@@ -891,9 +893,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       }
       group_sync();
       // ---- O^T += V^T P^T for this warp's channels, over the step's tiles
-#pragma unroll 1
-      for (int u = 0; u < 4 && k + u < end; ++u) {
-        if (*reinterpret_cast<volatile int*>(&key_of[4 * st + u]) < 0) continue;  // nothing was fetched
+      auto add_values = [&](int u) {
         const uint32_t vb = ring_s + st * C::kStepBytes + u * C::kTileBytes + L::kV;
         uint32_t ph[NR][2], pl[NR][2];
 #pragma unroll
@@ -933,6 +933,19 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
             if constexpr (PP == 2) mma_f16(racc[n], m01, 0u, m89, 0u, pl[n][0], pl[n][1]);
           }
         }
+      };
+      int4 keys;  // of the step's tiles
+      asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(keys.x), "=r"(keys.y), "=r"(keys.z), "=r"(keys.w)
+                   : "r"(smem_u32(key_of + 4 * st)));
+      if (k + 4 <= end && (keys.x | keys.y | keys.z | keys.w) >= 0) {
+        // all four are there: their loads and decoding overlap
+#pragma unroll
+        for (int u = 0; u < 4; ++u) add_values(u);
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < 4 && k + u < end; ++u)
+          if (lds_int(&key_of[4 * st + u]) >= 0) add_values(u);
       }
     }
     k = end;
