@@ -93,9 +93,7 @@ struct BatchCfg {
   using L = SingleTileLayout<KF, VF>;
   static constexpr int kRowsPad = 8;
   static constexpr int kTileBytes = L::kBytes;
-  // the query's B fragments: [block][k-step][lane]
-  static constexpr int kQFragBytes = BatchParts<T>::kQ == 2 ? 16 : 8;
-  static constexpr int kQBytes = 16 * 32 * kQFragBytes;
+  static constexpr int kQBytes = BatchParts<T>::kQ * 8 * 32 * 16;  // the query's B fragments (load_qfrag)
   static constexpr int kFit = kBatchRoom / (kQBytes + 2 * kTileBytes);
   static constexpr int kGroups = kFit < 12 ? kFit : 12;
   static constexpr int kStagesFit = (kBatchRoom / kGroups - kQBytes) / kTileBytes;
@@ -108,7 +106,7 @@ struct BatchCfg {
   static_assert(kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
   static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
   // What a unit costs beside its tiles, and the least a group takes, in tiles.
-  static constexpr int kUnitCost = 2, kMinShare = 4;
+  static constexpr int kUnitCost = 2, kMinShare = 2;
   static constexpr int kPair = 2;
 };
 
@@ -126,8 +124,8 @@ struct WideCfg {
   using L = SingleTileLayout<KF, VF>;
   static constexpr int kRowsPad = 8 * NR;
   static constexpr int kTileBytes = L::kBytes;
-  static constexpr int kQFragBytes = BatchParts<T>::kQ == 2 ? 16 : 8, kPFragBytes = BatchParts<T>::kP == 2 ? 16 : 8;
-  static constexpr int kQTileBytes = 16 * 32 * kQFragBytes;   // of one n-tile
+  static constexpr int kPFragBytes = BatchParts<T>::kP == 2 ? 16 : 8;
+  static constexpr int kQTileBytes = BatchParts<T>::kQ * 8 * 32 * 16;  // of one n-tile
   static constexpr int kPTileBytes = NR * 32 * kPFragBytes;   // of one tile of tokens
   static constexpr int kFixed = NR * kQTileBytes + 4 * kPTileBytes + sizeof(WideState<NR>);
   static constexpr int kStepBytes = 4 * kTileBytes;
@@ -299,6 +297,23 @@ __device__ __forceinline__ bool plan_stretches(const BatchDecodeParams& p, Batch
   return true;
 }
 
+__device__ __forceinline__ void sts128(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// The fragments that query_fragments stored for block bl.
+template <int QP>
+__device__ __forceinline__ void load_qfrag(uint32_t q_s, int bl, int lane, uint4 (&f)[2]) {
+  if constexpr (QP == 2) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) f[ks] = lds128(q_s + ((bl * 2 + ks) * 32 + lane) * 16);
+  } else {
+    const uint4 v = lds128(q_s + (bl * 32 + lane) * 16);
+    f[0] = make_uint4(v.x, v.y, 0u, 0u);
+    f[1] = make_uint4(v.z, v.w, 0u, 0u);
+  }
+}
+
 // The B fragments of query rows 8 nt .. + 7 of the unit, to shared memory (one warp).  A row is scaled by
 // the power of two that puts its largest magnitude into [1, 2) (exact), and split into f16 parts.
 // Returns what turns a dot product with scaled row g into a base-2 score; zero-point keys: the
@@ -306,7 +321,6 @@ __device__ __forceinline__ bool plan_stretches(const BatchDecodeParams& p, Batch
 template <typename T, int QP, bool KMIN, typename Between>
 __device__ __forceinline__ float query_fragments(const BatchDecodeParams& p, const BatchUnit& un, int nt, int lane,
                                                  uint32_t q_s, uint32_t& qsb_hi, uint32_t& qsb_lo, Between between) {
-  constexpr int kFragBytes = QP == 2 ? 16 : 8;
   const int g = lane >> 2, t = lane & 3;
   const int r = nt * 8 + g;
   Raw8<T> raw[kBlocks];
@@ -344,18 +358,18 @@ __device__ __forceinline__ float query_fragments(const BatchDecodeParams& p, con
     float xv[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) xv[e] = x[bl][e] * inv;
+    uint32_t hi[2][2], lo[2][2];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      uint32_t hi[2], lo[2];
-      split_pair(xv[4 * ks], xv[4 * ks + 1], hi[0], lo[0]);
-      split_pair(xv[4 * ks + 2], xv[4 * ks + 3], hi[1], lo[1]);
-      const uint32_t to = q_s + ((bl * 2 + ks) * 32 + lane) * kFragBytes;
-      if constexpr (QP == 2)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(lo[0]),
-                     "r"(lo[1])
-                     : "memory");
-      else
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(hi[0]), "r"(hi[1]) : "memory");
+      split_pair(xv[4 * ks], xv[4 * ks + 1], hi[ks][0], lo[ks][0]);
+      split_pair(xv[4 * ks + 2], xv[4 * ks + 3], hi[ks][1], lo[ks][1]);
+    }
+    // 16 bytes a lane: a k-step's high and low parts, or with one part both k-steps'
+    if constexpr (QP == 2) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) sts128(q_s + ((bl * 2 + ks) * 32 + lane) * 16, hi[ks][0], hi[ks][1], lo[ks][0], lo[ks][1]);
+    } else {
+      sts128(q_s + (bl * 32 + lane) * 16, hi[0][0], hi[0][1], hi[1][0], hi[1][1]);
     }
     if constexpr (KMIN) {
       float sm = 0.f;
@@ -523,16 +537,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
     }
     __syncwarp();
     // a fragment is read by the lane that wrote it
-    auto qfrag = [&](int bl, int ks) -> uint4 {
-      const uint32_t from = q_s + ((bl * 2 + ks) * 32 + lane) * C::kQFragBytes;
-      if constexpr (QP == 2) {
-        return lds128(from);
-      } else {
-        uint2 v;
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from));
-        return make_uint4(v.x, v.y, 0u, 0u);
-      }
-    };
+    auto qfrag = [&](int bl, uint4 (&f)[2]) { load_qfrag<QP>(q_s, bl, lane, f); };
 
     // ---- the tiles
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
@@ -787,16 +792,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
         }
         tile_scores<L, KF, VF, QP, NR, C::kPair>(
             kb, 0, g, t,
-            [&](int n, int bl, int ks) -> uint4 {
-              const uint32_t from = q_s + n * C::kQTileBytes + ((bl * 2 + ks) * 32 + lane) * C::kQFragBytes;
-              if constexpr (QP == 2) {
-                return lds128(from);
-              } else {
-                uint2 v;
-                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from));
-                return make_uint4(v.x, v.y, 0u, 0u);
-              }
-            },
+            [&](int n, int bl, uint4 (&f)[2]) { load_qfrag<QP>(q_s + n * C::kQTileBytes, bl, lane, f); },
             [&](int n) { return state->qsums[n][lane]; }, sv);
         const bool need_mask = key + 15 > pos0 || key <= last - span;
 #pragma unroll
@@ -1031,14 +1027,27 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
   }
 }
 
-// Merges the partials of the units that more than one group took part in.  One CTA per unit (and
-// per row, where there are few units), 256 threads = four groups of 64 (four channels each); a
-// group takes every fourth part, loading a batch of them before using any, and the groups are
-// combined once through shared memory.
-constexpr int kBatchMergeAhead = 8;
+// Merges the partials of the units that more than one group took part in: row blockIdx.y, +
+// gridDim.y, ... of unit blockIdx.x.  With few parts a warp takes a row (eight channels a lane, every
+// part loaded before any is used); with many the CTA does, its four groups of 64 threads taking
+// every fourth part, kMergeAhead loaded ahead (8 with four CTAs per SM, or 16 where the CTAs are few
+// and each may have over a hundred parts), combined once through shared memory.
+constexpr int kMergeFew = 4;
 
-template <typename T>
-__global__ void __launch_bounds__(256) merge_batch_kernel(const BatchDecodeParams p, int rows_pad) {
+// The store of a merged row: L = sum of exp2(lse_i - M), 0 where no part saw a key.
+__device__ __forceinline__ void store_lse(const BatchDecodeParams& p, const BatchUnit& un, int row, float M, float L) {
+  const int qi = row / p.group, hq = un.h * p.group + row - qi * p.group;
+  p.lse[static_cast<long long>(un.r0 + qi) * (p.b.n_kv * p.group) + hq] =
+      L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+}
+
+__device__ __forceinline__ long long out_row(const BatchDecodeParams& p, const BatchUnit& un, int row) {
+  const int qi = row / p.group, hq = un.h * p.group + row - qi * p.group;
+  return (un.r0 + qi) * p.out.row_stride + hq * p.out.head_stride;
+}
+
+template <typename T, int kMergeAhead, int kMinBlocks>
+__global__ void __launch_bounds__(256, kMinBlocks) merge_batch_kernel(const BatchDecodeParams p, int rows_pad) {
   __shared__ float red_m[4], red_l[4];
   __shared__ float4 red_o[4][kHeadDim / 4];
   const int u = blockIdx.x;
@@ -1050,23 +1059,56 @@ __global__ void __launch_bounds__(256) merge_batch_kernel(const BatchDecodeParam
   const int2 parts = p.unit_parts[u];
   const int c0 = parts.x >> 1, n_parts = parts.y - c0 + 1;
   if (n_parts == 1) return;  // written by its group
-  const int tid = threadIdx.x, grp = tid >> 6, d4 = tid & 63;
-  for (int row = blockIdx.y; row < un.rows * p.group; row += gridDim.y) {
+  const int tid = threadIdx.x, n_rows = un.rows * p.group;
+  auto part = [&](int i, int row) { return static_cast<long long>(i == 0 ? parts.x : 2 * (c0 + i)) * rows_pad + row; };
+  if (n_parts <= kMergeFew) {
+    const int lane = tid & 31;
+    for (int row = blockIdx.y + gridDim.y * (tid >> 5); row < n_rows; row += 8 * gridDim.y) {
+      float v[kMergeFew], x[kMergeFew][8];
+#pragma unroll
+      for (int i = 0; i < kMergeFew; ++i) {
+        v[i] = -INFINITY;
+        if (i < n_parts) {
+          v[i] = p.part_lse[part(i, row)];
+          load8<float>(p.part_o, part(i, row) * kHeadDim + 8 * lane, x[i]);
+        }
+      }
+      float M = -INFINITY, L = 0.f, r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kMergeFew; ++i) M = fmaxf(M, v[i]);
+      const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int i = 0; i < kMergeFew; ++i) {
+        if (i >= n_parts) break;
+        const float w = fast_exp2(v[i] - mu);  // 0 for a part that saw no key, NaN for a NaN part
+        L += w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] += w * x[i][e];
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] *= inv;
+      store8<T>(p.out.data, out_row(p, un, row) + 8 * lane, r);
+      if (lane == 0) store_lse(p, un, row, M, L);
+    }
+    return;
+  }
+  const int grp = tid >> 6, d4 = tid & 63;
+  for (int row = blockIdx.y; row < n_rows; row += gridDim.y) {
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = grp; i0 < n_parts; i0 += 4 * kBatchMergeAhead) {
-      float v[kBatchMergeAhead];
-      float4 o[kBatchMergeAhead];
+    for (int i0 = grp; i0 < n_parts; i0 += 4 * kMergeAhead) {
+      float v[kMergeAhead];
+      float4 o[kMergeAhead];
 #pragma unroll
-      for (int k = 0; k < kBatchMergeAhead; ++k) {
+      for (int k = 0; k < kMergeAhead; ++k) {
         const int i = i0 + 4 * k;
-        const long long at = static_cast<long long>(i == 0 ? parts.x : 2 * (c0 + i)) * rows_pad + row;
-        v[k] = i < n_parts ? p.part_lse[at] : -INFINITY;
-        o[k] = i < n_parts ? *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + 4 * d4)
+        v[k] = i < n_parts ? p.part_lse[part(i, row)] : -INFINITY;
+        o[k] = i < n_parts ? *reinterpret_cast<const float4*>(p.part_o + part(i, row) * kHeadDim + 4 * d4)
                            : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int k = 0; k < kBatchMergeAhead; ++k) {
+      for (int k = 0; k < kMergeAhead; ++k) {
         if (v[k] == -INFINITY) continue;  // a part that saw no key
         if (v[k] > m) {
           const float a = fast_exp2(m - v[k]);  // 0 when m = -inf
@@ -1099,17 +1141,14 @@ __global__ void __launch_bounds__(256) merge_batch_kernel(const BatchDecodeParam
         r.x += w * o.x; r.y += w * o.y; r.z += w * o.z; r.w += w * o.w;
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;
-      const int qi = row / p.group, hq = un.h * p.group + row - qi * p.group;
-      const long long at = (un.r0 + qi) * p.out.row_stride + hq * p.out.head_stride + 4 * d4;
+      const long long at = out_row(p, un, row) + 4 * d4;
       if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float4*>(static_cast<float*>(p.out.data) + at) =
             make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
       else
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out.data) + at) =
             make_uint2(pack2<T>(r.x * inv, r.y * inv), pack2<T>(r.z * inv, r.w * inv));
-      if (d4 == 0)
-        p.lse[static_cast<long long>(un.r0 + qi) * (p.b.n_kv * p.group) + hq] =
-            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+      if (d4 == 0) store_lse(p, un, row, M, L);
     }
     __syncthreads();
   }
@@ -1139,10 +1178,15 @@ static cudaError_t launch_batch_t(void (*kernel)(BatchDecodeParams), const Batch
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(units), units <= 296 ? std::min(p.group * p.b.max_rows, 24) : 1);
+  // as many CTAs per unit as are resident together, between one per row (few units: each may have
+  // many parts) and one per eight rows
+  const int rows = p.group * p.b.max_rows;
+  const long long per_unit = std::max<long long>(8ll * sms / units, (rows + 7) / 8);
+  cfg.gridDim = dim3(static_cast<unsigned>(units), static_cast<unsigned>(std::min<long long>(rows, per_unit)));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, merge_batch_kernel<T>, p, C::kRowsPad);
+  return units * rows <= sms ? cudaLaunchKernelEx(&cfg, merge_batch_kernel<T, 16, 1>, p, C::kRowsPad)
+                             : cudaLaunchKernelEx(&cfg, merge_batch_kernel<T, 8, 4>, p, C::kRowsPad);
 }
 
 #define KVATTN_BATCH_PAIRS(X)                                                                         \

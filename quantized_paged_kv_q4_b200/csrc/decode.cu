@@ -342,9 +342,10 @@ __global__ void __launch_bounds__(DecodeCfg<KF, VF, NT>::kThreads, 1) decode_ker
     qpos_min = min(qpos_min, __shfl_xor_sync(0xffffffffu, qpos_min, 1));
     qpos_min = min(qpos_min, __shfl_xor_sync(0xffffffffu, qpos_min, 2));
 
-    // the B fragments (hi0, hi1, lo0, lo1) of block bl, k-step ks
-    auto qfrag = [&](int bl, int ks) -> uint4 {
-      return lds128(q_s + ((((bl * 2 + ks) * NT + nt0) * 32 + lane) * 16));
+    // the B fragments (hi0, hi1, lo0, lo1) of block bl, both k-steps
+    auto qfrag = [&](int bl, uint4 (&f)[2]) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) f[ks] = lds128(q_s + ((((bl * 2 + ks) * NT + nt0) * 32 + lane) * 16));
     };
 
     // The CTA's tiles in increasing order, group grp taking k = grp, grp + kGroups, ... (the

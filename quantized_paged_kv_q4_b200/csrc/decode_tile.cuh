@@ -103,7 +103,7 @@ struct SingleTileLayout {
 // S = K Q^T of one tile of 16 tokens and NR n-tiles of 8 query rows (one warp; g = lane / 4, t = lane %
 // 4): sacc[n][e] is token g + 8 (e / 2), row 2t + e % 2 of n-tile n.
 //   QP             f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
-//   qfrag(n, b, ks) the B fragments of n-tile n, block b, k-step ks (hi0, hi1, lo0, lo1)
+//   qfrag(n, b, f) fills f[k-step] with the B fragments of n-tile n, block b (hi0, hi1, lo0, lo1)
 //   qsums(n)       zero-point keys: the query's block sums as a B fragment (hi, lo)
 //   PAIR           blocks whose MMAs are interleaved (1 or 2: 2 takes 8 + 4 more registers)
 // The tile is tile G of the copy at kb, arranged as L.
@@ -144,21 +144,22 @@ __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QF
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       float xb[PAIR][4];
+      uint4 f[PAIR][2];
+#pragma unroll
+      for (int i = 0; i < PAIR; ++i) qfrag(n, bl + i, f[i]);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        uint4 f[PAIR];
-#pragma unroll
-        for (int i = 0; i < PAIR; ++i) f[i] = qfrag(n, bl + i, ks);
 #pragma unroll
         for (int i = 0; i < PAIR; ++i) {
           if (ks == 0)
-            mma_f16_z(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i].x, f[i].y);
+            mma_f16_z(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i][ks].x, f[i][ks].y);
           else
-            mma_f16(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i].x, f[i].y);
+            mma_f16(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i][ks].x, f[i][ks].y);
         }
         if constexpr (QP == 2) {
 #pragma unroll
-          for (int i = 0; i < PAIR; ++i) mma_f16(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i].z, f[i].w);
+          for (int i = 0; i < PAIR; ++i)
+            mma_f16(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i][ks].z, f[i][ks].w);
         }
       }
 #pragma unroll
@@ -302,7 +303,7 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g
 // Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
 // lane % 4; the thread's rows are 2t, 2t + 1).
 //   QP, PP       f16 parts of the query and of P: 2 keeps about 22 bits of each, 1 rounds once
-//   qfrag(b, ks) the query's B fragments of block b, k-step ks (hi0, hi1, lo0, lo1)
+//   qfrag(b, f)  fills f[k-step] with the query's B fragments of block b (hi0, hi1, lo0, lo1)
 //   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment
 //   crow         turns a dot product with the normalised row into a base-2 softmax score
 //   grow         how far, in powers of two, a score may pass the running maximum (p <= 2^grow)
@@ -316,7 +317,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
   using F = TileFormat<KF, VF>;
   float sacc[1][4];
   tile_scores<L, KF, VF, QP, 1, PAIR>(
-      kb, G, g, t, [&](int, int bl, int ks) { return qfrag(bl, ks); }, [&](int) { return make_uint2(qsb_hi, qsb_lo); },
+      kb, G, g, t, [&](int, int bl, uint4 (&f)[2]) { qfrag(bl, f); }, [&](int) { return make_uint2(qsb_hi, qsb_lo); },
       sacc);
   // ---------------- online softmax (base 2) ----------------
   // The running maximum m_run of a row is shared by the 8 lanes that hold the row.
