@@ -490,11 +490,14 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
  *                NULL without page_logical: as many as the sequence has blocks; NULL with it:
  *                max_blocks
  *   window       0: every key up to the row's own position
- *   out          [n_rows][H_q][256] of q's dtype: softmax(q.k/16) v
+ *   out          [n_rows][H_q][256] of q's dtype: softmax(q.k/16) v; may be q's own array
  *   lse          device fp32 [n_rows][H_q]: as for kvattn_decode (a row that sees no key: -inf,
  *                out = 0)
  *   ws           device workspace of kvattn_decode_batch_workspace_size() bytes, 256-byte
  *                aligned; needs no initialisation.  Calls that share one must not overlap.
+ * Accuracy: fp32 and fp16 as kvattn_decode (about 2^-20 relative before fp16's own rounding).  With
+ * bf16, P and P x the value's scale are rounded to f16 (2^-12 each, of what is summed) before the
+ * 2^-9 of the output's rounding.
  * Supports group * max_rows <= 24 and n_seqs * H_kv * max_blocks <= 2^27 (table entries).
  * Results do not depend on timing: the split of the work depends on the lengths and the device
  * alone. */

@@ -103,9 +103,8 @@ struct BatchSeq {
   int r0, rows, pos0;
 };
 
-__device__ __forceinline__ BatchSeq load_seq(const BatchParams& p, int s, bool check_blocks) {
+__device__ __forceinline__ BatchSeq check_seq(const BatchParams& p, int r0, int r1, int pos0, bool check_blocks) {
   BatchSeq q;
-  const int r0 = p.row_start[s], r1 = p.row_start[s + 1], pos0 = p.pos_start[s];
   const long long end = static_cast<long long>(pos0) + (static_cast<long long>(r1) - r0);
   const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.n_rows && static_cast<long long>(r1) - r0 <= p.max_rows && pos0 >= 0 &&
                   end <= INT32_MAX &&
@@ -115,6 +114,10 @@ __device__ __forceinline__ BatchSeq load_seq(const BatchParams& p, int s, bool c
   q.pos0 = pos0;
   if (!ok) record_error(KVATTN_ERR_INVALID_ARG);
   return q;
+}
+
+__device__ __forceinline__ BatchSeq load_seq(const BatchParams& p, int s, bool check_blocks) {
+  return check_seq(p, p.row_start[s], p.row_start[s + 1], p.pos_start[s], check_blocks);
 }
 
 }  // namespace kvattn

@@ -28,26 +28,40 @@ struct TileRows {
 
 // Tile slots: sequence s owns slots row_start[s] / 16 + 2 s ..., at least as many as its rows touch
 // tiles, so a slot's sequence is found by a search without any prefix sum.
-__device__ __forceinline__ long long slot_base(const int32_t* row_start, int s) {
-  return (static_cast<long long>(row_start[s]) >> 4) + 2ll * s;
-}
+__device__ __forceinline__ long long slot_base(int r0, int s) { return (static_cast<long long>(r0) >> 4) + 2ll * s; }
 
 __device__ __forceinline__ bool locate_tile(const BatchParams& p, long long at, int h, int lane, TileRows* out) {
   // the last sequence whose slots start at or before `at`, 32 candidates a step; whatever row_start
-  // holds, the answer stays inside [0, n_seqs) and is checked below
+  // holds, the answer stays inside [0, n_seqs) and is checked below.  In the last step the lanes
+  // load the rest of their candidates too, so that the answer's is there at once.
   int lo = 0, hi = p.n_seqs;
+  BatchSeq q;
+  long long base;
   while (true) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + lane * step;
-    const uint32_t le = __ballot_sync(0xffffffffu, i < hi && slot_base(p.row_start, i) <= at);
+    int r0 = 0, r1 = 0, pos0 = 0;
+    if (i < hi) {
+      r0 = p.row_start[i];
+      if (step == 1) {
+        r1 = p.row_start[i + 1];
+        pos0 = p.pos_start[i];
+      }
+    }
+    const uint32_t le = __ballot_sync(0xffffffffu, i < hi && slot_base(r0, i) <= at);
     if (le == 0) return false;
-    lo += (31 - __clz(le)) * step;
+    const int found = 31 - __clz(le);
+    lo += found * step;
     hi = min(hi, lo + step);
-    if (step == 1) break;
+    if (step == 1) {
+      r0 = __shfl_sync(0xffffffffu, r0, found);
+      base = slot_base(r0, lo);
+      q = check_seq(p, r0, __shfl_sync(0xffffffffu, r1, found), __shfl_sync(0xffffffffu, pos0, found), true);
+      break;
+    }
   }
-  const BatchSeq q = load_seq(p, lo, true);
   if (q.rows == 0) return false;
-  const long long tile = q.pos0 / 16 + (at - slot_base(p.row_start, lo));
+  const long long tile = q.pos0 / 16 + (at - base);
   const long long first = max(tile * 16, static_cast<long long>(q.pos0));
   const long long end = min(tile * 16 + 16, static_cast<long long>(q.pos0) + q.rows);
   if (tile < q.pos0 / 16 || first >= end) return false;

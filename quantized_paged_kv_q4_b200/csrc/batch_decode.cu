@@ -385,11 +385,11 @@ __device__ __forceinline__ float query_fragments(const BatchDecodeParams& p, con
   return __uint_as_float(static_cast<uint32_t>(ex) << 23) * (1.0f / 16.0f) * 1.4426950408889634f;
 }
 
-// Entry i of unit u's list: page (-2: none there) and logical block.
+// Entry i of unit u's list: page and logical block (-1: no such entry).
 __device__ __forceinline__ int2 page_of(const BatchDecodeParams& p, int u, int i) {
   const long long at = static_cast<long long>(u) * p.b.max_blocks + i;
   const bool any = i < p.b.max_blocks && (!p.n_list || i < p.n_list[u]);
-  return make_int2(any ? p.b.page_table[at] : -2, any && p.page_logical ? p.page_logical[at] : i);
+  return make_int2(any ? p.b.page_table[at] : 0, !any ? -1 : p.page_logical ? p.page_logical[at] : i);
 }
 
 // Makes w the unit of the warp's copying, its first tile at `start`.
@@ -408,7 +408,7 @@ __device__ __forceinline__ void producer_unit(const BatchDecodeParams& p, Produc
 
 // Whether block e.y with page id e.x holds a key that some row sees (a bad id of such a block is recorded).
 __device__ __forceinline__ bool fetch_block(const BatchDecodeParams& p, int2 e, int last, int low, int lane) {
-  if (e.x == -2 || e.y < 0 || e.y > last / kPageTokens || e.y < low / kPageTokens) return false;
+  if (e.y < 0 || e.y > last / kPageTokens || e.y < low / kPageTokens) return false;
   if (e.x >= 0 && e.x < p.b.n_pages) return true;
   if (lane == 0) record_error(KVATTN_ERR_BAD_PAGE);
   return false;
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
     }
     __syncwarp();
   };
-  int2 ahead = make_int2(-2, 0);  // the entry after the page at hand, loaded when that was opened
+  int2 ahead = make_int2(0, -1);  // the entry after the page at hand, loaded when that was opened
   // starts the copies of tile k; one group of copies per call, an empty one past the end
   auto issue = [&](int k) {
     if (k < n_tiles) {
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
     uint32_t qsb_hi = 0u, qsb_lo = 0u;
     {
       // every load before any use: the first two pages, then the query rows
-      int2 here = make_int2(-2, 0);
+      int2 here = make_int2(0, -1);
       if (k == 0) {
         const int i = (un.t0 - start) >> 3;
         here = page_of(p, un.unit, i);
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
   Producer* prod = &plan->producer[warp];
   auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory"); };
 
-  int2 ahead = make_int2(-2, 0);  // this warp's entry of the next step to be copied, loaded a step ahead
+  int2 ahead = make_int2(0, -1);  // this warp's entry of the next step to be copied, loaded a step ahead
   // starts the copies of this warp's tile of the next step into stage st, and moves on
   auto issue = [&](int st) {
     const int k0 = lds_int(&prod->next);

@@ -126,6 +126,10 @@ def test_decode_refusals(lib):
     assert calls(lib, d, b, ws_bytes=need - 1)["decode"] == kvattn.ERR_WORKSPACE_TOO_SMALL
     assert calls(lib, d, batch(max_rows=5))["decode"] == SHAPE       # 6 query heads x 5 rows > 24
     assert calls(lib, desc(n_kv_heads=1, n_q_heads=25), batch(max_rows=1))["decode"] == SHAPE
+    # the line of tiles is counted in 32 bits: n_seqs x H_kv x max_blocks <= 2^27
+    assert calls(lib, d, batch(n_seqs=1 << 13, max_blocks=1 << 12, max_rows=1))["decode"] in (
+        kvattn.ERR_NOT_INITIALIZED, kvattn.ERR_CUDA)
+    assert calls(lib, d, batch(n_seqs=1 << 13, max_blocks=(1 << 12) + 1, max_rows=1))["decode"] == SHAPE
     for kf, vf in (("q5_0", "q4_0"), ("q8_0", "q4_1")):
         assert set(calls(lib, desc(k_fmt=kf, v_fmt=vf), b).values()) == {FORMAT}
 

@@ -278,6 +278,106 @@ def test_decode_peaked_scores(kv_gpu):
         check_decode(c, name, *run_decode(kv_gpu, c, name, q_scale=8.0))
 
 
+def test_decode_in_place_and_on_few_sms(kv_gpu):
+    """out may be q's array; a descriptor's SM budget sizes the grid (other splits, the same answer)."""
+    import torch
+
+    for lens, group in (([(2000, 1), (3, 1), (700, 1)], 6), ([(2000, 4), (3, 2), (700, 3)], 6)):
+        c = BatchCache(lens, 2, group, "q8_0", "q4_0", 51).on_gpu(kv_gpu)
+        for budget in (0, 3, 40):
+            c.desc.sm_budget = budget
+            qx, q = rounded(np.random.default_rng(1).standard_normal((c.total, 2 * group, 256)).astype(np.float32), "float32")
+            lse = torch.zeros((c.total, 2 * group), device="cuda")
+            ws = torch.empty(kv_gpu.kvattn_decode_batch_workspace_size(c.desc, c.batch), dtype=torch.uint8, device="cuda")
+            kv_gpu.kvattn_decode_batch(c.desc, c.batch, q, q, lse, ws)
+            check_decode(c, "float32", qx, q.cpu().numpy(), lse.cpu().numpy())
+    assert kv_gpu.kvattn_device_error() == 0
+
+
+def test_decode_nan_and_inf_queries_stay_in_their_row(kv_gpu):
+    import torch
+
+    for lens in ([(40, 1), (3000, 1)], [(40, 2), (3000, 3)]):
+        for name in TYPES:
+            c = BatchCache(lens, 1, 6, "q8_0", "q4_0", 52).on_gpu(kv_gpu)
+            qx, q = rounded(np.random.default_rng(2).standard_normal((c.total, 6, 256)).astype(np.float32), name)
+            bad = [(0, 2, 7, float("nan")), (c.total - 1, 5, 250, float("inf"))]
+            for r, h, ch, x in bad:
+                q[r, h, ch] = x
+            out, lse = torch.zeros_like(q), torch.zeros((c.total, 6), device="cuda")
+            ws = torch.empty(kv_gpu.kvattn_decode_batch_workspace_size(c.desc, c.batch), dtype=torch.uint8, device="cuda")
+            kv_gpu.kvattn_decode_batch(c.desc, c.batch, q, out, lse, ws)
+            o, l = out.float().cpu().numpy(), lse.cpu().numpy()
+            for r, h, _, _ in bad:
+                assert np.isnan(o[r, h]).all() and np.isnan(l[r, h])
+                # the row's own place aside, the answer is that of the clean queries
+                o[r, h], l[r, h] = 0, 0
+            assert np.isfinite(o).all() and np.isfinite(l).all()
+            out2, lse2 = torch.zeros_like(q), torch.zeros_like(lse)
+            kv_gpu.kvattn_decode_batch(c.desc, c.batch, torch.from_numpy(qx).to(q), out2, lse2, ws)
+            o2, l2 = out2.float().cpu().numpy(), lse2.cpu().numpy()
+            for r, h, _, _ in bad:
+                o2[r, h], l2[r, h] = 0, 0
+            assert np.array_equal(o, o2) and np.array_equal(l, l2)
+    assert kv_gpu.kvattn_device_error() == 0
+
+
+def test_two_streams_and_two_graphs(kv_gpu):
+    """Calls on two streams at once with a workspace each; two captured graphs that share one workspace,
+    replayed in turn; lengths that change between replays."""
+    import torch
+
+    kv = kv_gpu
+    a = BatchCache([(900, 1), (50, 1), (4000, 1)], 2, 6, "q8_0", "q4_0", 53).on_gpu(kv)
+    b = BatchCache([(300, 4), (1200, 2)], 2, 6, "q4_0", "q4_0", 54).on_gpu(kv)
+    sets = []
+    for c, name, seed in ((a, "bfloat16", 1), (b, "float32", 2)):
+        qx, q = rounded(np.random.default_rng(seed).standard_normal((c.total, 12, 256)).astype(np.float32), name)
+        size = kv.kvattn_decode_batch_workspace_size(c.desc, c.batch)
+        sets.append([c, name, qx, q, torch.zeros_like(q), torch.zeros((c.total, 12), device="cuda"), size])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    own_ws = [torch.empty(s[6], dtype=torch.uint8, device="cuda") for s in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, ws, st in zip(sets, own_ws, streams):
+            kv.kvattn_decode_batch(s[0].desc, s[0].batch, s[3], s[4], s[5], ws, stream=st)
+    torch.cuda.synchronize()
+    for c, name, qx, _, out, lse, _ in sets:
+        check_decode(c, name, qx, out.float().cpu().numpy(), lse.cpu().numpy())
+    shared = torch.empty(max(s[6] for s in sets), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c, _, _, q, out, lse, _ in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kv.kvattn_decode_batch(c.desc, c.batch, q, out, lse, shared)
+        graphs.append(g)
+    for _ in range(3):
+        for s in sets:
+            s[4].zero_()
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for c, name, qx, _, out, lse, _ in sets:
+        check_decode(c, name, qx, out.float().cpu().numpy(), lse.cpu().numpy())
+    # the first graph again, with its sequences cut short
+    a.t_pos.copy_(torch.tensor([100, 0, 2500], dtype=torch.int32))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    a.lens = [(100, 1), (0, 1), (2500, 1)]
+    for s in range(3):
+        a.k[s], a.v[s] = a.k[s][:sum(a.lens[s])], a.v[s][:sum(a.lens[s])]
+    check_decode(a, "bfloat16", sets[0][2], sets[0][4].float().cpu().numpy(), sets[0][5].cpu().numpy())
+    assert kv.kvattn_device_error() == 0
+
+
+@pytest.mark.parametrize("group,rows", [(6, 1), (6, 3)])
+def test_decode_long_and_short_together(kv_gpu, group, rows):
+    """One long sequence among many single tokens: stretches that hold many units, units of many parts."""
+    lens = [(0, 1)] * 60 + [(9000, rows)] + [(0, 0)] * 40 + [(int(i), 1) for i in range(37)]
+    c = BatchCache(lens, 1, group, "q8_0", "q4_0", 55)
+    check_decode(c, "bfloat16", *run_decode(kv_gpu, c, "bfloat16"))
+
+
 # ------------------------------------------------------------------------- device checks
 def test_bad_sequences_and_pages_are_left_out(kv_gpu):
     import torch
@@ -331,7 +431,7 @@ def test_bad_page_ids_are_skipped(kv_gpu):
     c = BatchCache([(300, 2), (40, 1)], 1, 6, "q8_0", "q4_0", 32).on_gpu(kv)
     table = c.table.copy()
     table[0, 0, 1] = c.n_phys
-    table[1, 0, 0] = -1
+    table[1, 0, 0] = -2
     c.t_table.copy_(torch.from_numpy(table))
     q = torch.randn((3, 6, 256), device="cuda")
     out, lse = torch.full_like(q, 7.0), torch.full((3, 6), 7.0, device="cuda")
