@@ -1,15 +1,23 @@
 // The cache of a ragged batch, written and read back (kvattn_append_batch, kvattn_read_batch).
 //
 // One warp takes a quarter (64 channels of K and of V) of one (tile of 16 positions of a sequence, KV
-// head): a whole tile a warp left a prompt of a few thousand tokens with too few warps (49.8 us for
-// six prompts against TWO).  A page's codes and scales sit
-// in tensor-core fragment order by such tiles, so a tile is a few contiguous ranges of the page, and
-// lane (g, t) = (lane / 4, lane % 4) of a warp that holds rows 8H + g, channels 32b + 8t .. + 7 of
-// every block b holds, block by block, exactly the keys' bytes it stores: 16 of them per 64
-// channels.  The four lanes of a quad form one 32-channel block, as in the single-sequence encoder.
-// Values are stored transposed (a lane's bytes belong to four tokens), which takes four shuffles
-// per block and eight tokens.  Both directions are bound by HBM: a bf16 tile is 16,384 bytes of rows
-// and 6,656 (Q8_0 / Q4_0) of page.
+// head).  A page's codes and scales sit in tensor-core fragment order by such tiles, so a tile is a
+// few contiguous ranges of the page, and lane (g, t) = (lane / 4, lane % 4) of a warp that holds rows
+// 8H + g, channels 32b + 8t .. + 7 of every block b holds, block by block, exactly the key bytes it
+// stores: 16 of them per 64 channels.  The four lanes of a quad form one 32-channel block, as in
+// the single-sequence encoder.  Values are stored transposed (a lane's bytes belong to four
+// tokens), which takes four shuffles per block and eight tokens.
+//
+// Reading is bound by HBM: 131,072 tokens of 4 KV heads (Q8_0 / Q4_0, 218 MB) into bf16 (537 MB)
+// take 124 us, 0.94 of the measured copy bandwidth.  Writing a whole tile costs about 1,250
+// instructions a quarter (scales by IEEE division and reciprocal, codes by the format's own fp32
+// steps): six prompts of 100 to 4,000 tokens (28 MB of bf16 rows, 8 MB of pages) take 19 us, a
+// third of the copy bandwidth, bound by instruction issue (0.64 per cycle) and by one and a half
+// waves of CTAs.  One to eight tokens take 3 us a call, latency alone.
+// Measured on the way: one warp per (row, head), with its byte stores and strided page reads: 215 us
+// for the 131,072 tokens; a whole tile a warp: 49.8 us to write the six prompts and read them back
+// (25.7 us in quarters).  Not kept: codes made by adding 2^23 with downward rounding and packed by
+// multiply-adds on the biased bits (the same bytes, 25.0 instead of 25.7 us).
 //
 // A tile that the call's rows fill in part is written token by token with byte stores (its other
 // tokens' bits share bytes and words with them, and stay).

@@ -24,6 +24,14 @@
 // a fixed order.  A group has at most two partials, its first unit's and its last's, so the
 // workspace has two slots per group.
 //
+// What bounds it.  With 8 rows and bf16 a tile takes a warp about 565 instructions, and twelve warps
+// a SM keep up with HBM: eight sequences of 131,072 tokens (1.745 GB, Q8_0 / Q4_0) take 270 to 285
+// us in short runs, 0.95 to 1.0 of the measured copy bandwidth, and 320 us in a run of half a second,
+// where the 1,000 W cap brings the SM clock to 1.57 GHz.  With 24 rows a tile takes 1,200
+// instructions at 0.46 a cycle (dependent instructions, shared-memory latency, the pace of mma.sync):
+// eight verify steps of four tokens (149 MB) take 63 us, 0.36.  Short batches are bound by latency: the
+// plan 2.4 us, pages and queries 3 us, then 1.5 to 2 us a tile and group, and the merge grid.
+//
 // Not kept: a CTA of four groups on one stretch, their states merged through shared memory at the
 // end of each unit (2 to 4 us of barriers a unit: 32 ragged sequences of up to 16,384 tokens in
 // 51.9 us, against 40.4); three warps per tile with 24 rows, one per n-tile (eight verify steps of
