@@ -447,7 +447,7 @@ typedef struct kvattn_rows {
  * batch) are neither read nor written.
  * Checked on the device, because the arrays live there: 0 <= row_start[s] <= row_start[s + 1]
  * <= n_rows, at most max_rows rows, pos_start[s] >= 0 and the last position inside max_blocks
- * blocks.  A sequence that breaks one of these is left out (none of its rows is written), and
+ * blocks (and below 2^31 - 128).  A sequence that breaks one of these is left out (none of its rows is written), and
  * where row_start does not ascend others may be too; KVATTN_ERR_INVALID_ARG is recorded in the
  * device error word. */
 typedef struct kvattn_batch {
@@ -456,7 +456,7 @@ typedef struct kvattn_batch {
   const int32_t* page_table; /* device int32 [n_seqs][H_kv][max_blocks]: logical block ->   */
                              /* physical page (entries no token needs are not read)         */
   int64_t n_rows;            /* rows of the token arrays, < 2^31                            */
-  int32_t n_seqs;
+  int32_t n_seqs;            /* n_seqs * H_kv <= 2^27                                       */
   int32_t max_rows;          /* the most rows of any sequence                               */
   int32_t max_blocks;
   int32_t reserved;          /* must be 0                                                   */

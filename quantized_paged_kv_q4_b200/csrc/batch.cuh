@@ -107,7 +107,7 @@ __device__ __forceinline__ BatchSeq check_seq(const BatchParams& p, int r0, int 
   BatchSeq q;
   const long long end = static_cast<long long>(pos0) + (static_cast<long long>(r1) - r0);
   const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.n_rows && static_cast<long long>(r1) - r0 <= p.max_rows && pos0 >= 0 &&
-                  end <= INT32_MAX &&
+                  end <= INT32_MAX - kPageTokens &&  // positions of a whole page never overflow
                   (!check_blocks || r1 == r0 || end <= static_cast<long long>(p.max_blocks) * kPageTokens);
   q.r0 = r0;
   q.rows = ok ? r1 - r0 : 0;
@@ -116,8 +116,10 @@ __device__ __forceinline__ BatchSeq check_seq(const BatchParams& p, int r0, int 
   return q;
 }
 
+// Read through L2: the decode's merge grid reads the arrays while the split grid before it still
+// runs, when what an earlier kernel wrote is in L2 but a line of this SM's L1 may be older.
 __device__ __forceinline__ BatchSeq load_seq(const BatchParams& p, int s, bool check_blocks) {
-  return check_seq(p, p.row_start[s], p.row_start[s + 1], p.pos_start[s], check_blocks);
+  return check_seq(p, __ldcg(p.row_start + s), __ldcg(p.row_start + s + 1), __ldcg(p.pos_start + s), check_blocks);
 }
 
 }  // namespace kvattn

@@ -17,7 +17,8 @@ int validate_batch(const kvattn_kv_desc* desc, const kvattn_batch* b) {
   if (b->n_seqs < 0 || b->n_rows < 0 || b->n_rows > INT32_MAX || b->max_rows < 0 || b->max_blocks < 0 ||
       b->max_blocks > (INT32_MAX / kPageTokens) + 1)
     return KVATTN_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(b->n_seqs) * desc->n_kv_heads > INT32_MAX) return KVATTN_ERR_UNSUPPORTED_SHAPE;
+  // units are searched and counted in 32 bits
+  if (static_cast<int64_t>(b->n_seqs) * desc->n_kv_heads > (1 << 27)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
   if (b->n_seqs > 0 && (!b->row_start || !b->pos_start || (b->max_blocks > 0 && !b->page_table)))
     return KVATTN_ERR_INVALID_ARG;
   return KVATTN_OK;

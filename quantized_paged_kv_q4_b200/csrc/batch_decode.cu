@@ -162,7 +162,7 @@ __device__ __forceinline__ int seq_first_tile(const BatchDecodeParams& p, const 
 // something that writes its rows), which may have no page behind it.
 __device__ __forceinline__ int unit_tiles(const BatchDecodeParams& p, const BatchSeq& q, long long unit) {
   if (q.rows == 0) return 0;
-  if (p.n_list) return max(1, 8 * min(max(p.n_list[unit], 0), p.b.max_blocks));
+  if (p.n_list) return max(1, 8 * min(max(__ldcg(p.n_list + unit), 0), p.b.max_blocks));
   if (p.page_logical) return max(1, 8 * p.b.max_blocks);
   return (q.pos0 + q.rows - 1) / 16 + 1 - seq_first_tile(p, q);
 }
@@ -1197,10 +1197,6 @@ static cudaError_t launch_batch_t(void (*kernel)(BatchDecodeParams), const Batch
                              : cudaLaunchKernelEx(&cfg, merge_batch_kernel<T, 8, 4>, p, C::kRowsPad);
 }
 
-#define KVATTN_BATCH_PAIRS(X)                                                                         \
-  X(kKeyQ8, kValQ4) X(kKeyQ8, kValQ8) X(kKeyQ4, kValQ4) X(kKeyQ4, kValQ8) X(kKeyQ51, kValQ4)            \
-  X(kKeyQ51, kValQ8) X(kKeyQ50, kValQ41)
-
 template <int KF, int VF, typename T>
 static cudaError_t launch_batch_rows(const BatchDecodeParams& p, int sms, long long most_tiles, cudaStream_t stream) {
   switch (batch_row_tiles(p.group * p.b.max_rows)) {
@@ -1219,7 +1215,7 @@ cudaError_t launch_decode_batch(const BatchDecodeParams& p, int dtype, int k_fmt
     return dtype == KVATTN_F32   ? launch_batch_rows<KF, VF, float>(p, sms, most_tiles, stream)           \
            : dtype == KVATTN_F16 ? launch_batch_rows<KF, VF, __half>(p, sms, most_tiles, stream)          \
                                  : launch_batch_rows<KF, VF, __nv_bfloat16>(p, sms, most_tiles, stream);
-  KVATTN_BATCH_PAIRS(KV_LAUNCH)
+  KVATTN_DECODE_PAIRS(KV_LAUNCH)
 #undef KV_LAUNCH
   return cudaErrorInvalidValue;
 }
@@ -1242,7 +1238,7 @@ cudaError_t prepare_batch_kernels() {
 #define KV_SET1(KF, VF, T) \
   if ((e = prepare_batch_t<KF, VF, T>()) != cudaSuccess) return e;
 #define KV_SET(KF, VF) KV_SET1(KF, VF, float) KV_SET1(KF, VF, __half) KV_SET1(KF, VF, __nv_bfloat16)
-  KVATTN_BATCH_PAIRS(KV_SET)
+  KVATTN_DECODE_PAIRS(KV_SET)
 #undef KV_SET
 #undef KV_SET1
   return cudaSuccess;

@@ -620,7 +620,7 @@ static cudaError_t launch_decode_t(const DecodeParams& prm, int n_kv, cudaStream
   return cudaLaunchKernelEx(&cfg, decode_kernel<KF, VF, NT>, prm);
 }
 
-// The supported (key, value) format pairs: Q8_0 keys with Q4_0 or Q8_0 values, Q4_0 and Q5_1
+// The supported (key, value) format pairs (of the ragged-batch decode too): Q8_0 keys with Q4_0 or Q8_0 values, Q4_0 and Q5_1
 // keys with Q4_0 or Q8_0 values, Q5_0 keys with Q4_1 values.
 #define KVATTN_DECODE_PAIRS(X) \
   X(kKeyQ8, kValQ4) X(kKeyQ8, kValQ8) X(kKeyQ4, kValQ4) X(kKeyQ4, kValQ8) X(kKeyQ51, kValQ4) \

@@ -13,6 +13,10 @@ from quantized_paged_kv_q4_b200 import build, kvattn
 
 @pytest.fixture(scope="module")
 def lib():
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("the addresses passed here are not memory: only where no device can be initialised")
     build.build()
     return kvattn.lib()
 
@@ -58,6 +62,12 @@ def test_good_arguments_reach_the_device_check(lib):
 def test_bad_batches(lib, kw):
     assert set(calls(lib, desc(), batch(**kw)).values()) == {INVALID}
     assert lib.kvattn_decode_batch_workspace_size(desc(), batch(**kw)) == 0
+
+
+def test_too_many_units(lib):
+    good = (kvattn.ERR_NOT_INITIALIZED, kvattn.ERR_CUDA)
+    assert all(st in good for st in calls(lib, desc(), batch(n_seqs=1 << 25, max_blocks=1)).values())
+    assert set(calls(lib, desc(), batch(n_seqs=(1 << 25) + 1, max_blocks=1)).values()) == {SHAPE}
 
 
 def test_null_arguments(lib):
