@@ -113,9 +113,10 @@ struct BatchCfg {
   static constexpr int kSmemBytes = kMetaOff + kBatchMeta;
   static_assert(kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
   static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
-  // What a unit costs beside its tiles, and the least a group takes, in tiles.
-  static constexpr int kUnitCost = 2, kMinShare = 2;
-  static constexpr int kPair = 2;
+  // What a unit costs beside its tiles, and the least a group takes, in tiles.  Units: 32 ragged
+  // sequences in 41.3 us with 2, 38.8 with 4.  Shares: 1 x 4,096 tokens in 17.1 us with 4, 15.0 with 2
+  // (128 groups of two tiles and a merge of 128 parts).
+  static constexpr int kUnitCost = 4, kMinShare = 2;
 };
 
 // The wide kernel's state of a unit, per group: rows in order.
@@ -148,8 +149,9 @@ struct WideCfg {
   static constexpr int kSmemBytes = kMetaOff + kBatchMeta;
   static_assert(kGroups >= 1 && kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
   static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
+  // 48 windowed sequences in 38.2, 35.6 and 37.8 us with (3, 4), (6, 8) and (10, 16), eight verify
+  // steps in 65.5, 63.5 and 62.2
   static constexpr int kUnitCost = 6, kMinShare = 8;
-  static constexpr int kPair = 2;
 };
 
 __device__ __forceinline__ int lds_int(const int* p) { return static_cast<int>(lds32(smem_u32(p))); }
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
-        attend_tile<L, KF, VF, QP, PP, C::kPair>(
+        attend_tile<L, KF, VF, QP, PP>(
             kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow, 2.f,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
@@ -798,7 +800,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           uint8_t* vs = ring + st * C::kStepBytes + w * C::kTileBytes + L::kV + L::kVScale;
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
-        tile_scores<L, KF, VF, QP, NR, C::kPair>(
+        tile_scores<L, KF, VF, QP, NR>(
             kb, 0, g, t,
             [&](int n, int bl, uint4 (&f)[2]) { load_qfrag<QP>(q_s + n * C::kQTileBytes, bl, lane, f); },
             [&](int n) { return state->qsums[n][lane]; }, sv);

@@ -105,9 +105,9 @@ struct SingleTileLayout {
 //   QP             f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
 //   qfrag(n, b, f) fills f[k-step] with the B fragments of n-tile n, block b (hi0, hi1, lo0, lo1)
 //   qsums(n)       zero-point keys: the query's block sums as a B fragment (hi, lo)
-//   PAIR           blocks whose MMAs are interleaved (1 or 2: 2 takes 8 + 4 more registers)
+// (Interleaving the MMAs of two blocks measured no faster in any kernel, for 12 more registers.)
 // The tile is tile G of the copy at kb, arranged as L.
-template <typename L, int KF, int VF, int QP, int NR, int PAIR, typename QFrag, typename QSums>
+template <typename L, int KF, int VF, int QP, int NR, typename QFrag, typename QSums>
 __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QFrag qfrag, QSums qsums,
                                             float (&sacc)[NR][4]) {
   using F = TileFormat<KF, VF>;
@@ -138,37 +138,21 @@ __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QF
       dkf[H][2 * e + 1] = half_hi(w[e]);
     }
   }
-  // PAIR blocks at a time: an MMA per k-step and query part into each one's xb, the blocks' in turn
-  // (their chains are independent), then S += d * xb
-  auto blocks_qk = [&](int bl, const uint32_t (&A)[PAIR][2][4]) {
+  // one block: an MMA per k-step and query part into xb, then S += d * xb
+  auto block_qk = [&](int bl, const uint32_t (&A)[2][4]) {
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      float xb[PAIR][4];
-      uint4 f[PAIR][2];
+      float xb[4];
+      uint4 f[2];
+      qfrag(n, bl, f);
+      mma_f16_z(xb, A[0][0], A[0][1], A[0][2], A[0][3], f[0].x, f[0].y);
+      if constexpr (QP == 2) mma_f16(xb, A[0][0], A[0][1], A[0][2], A[0][3], f[0].z, f[0].w);
+      mma_f16(xb, A[1][0], A[1][1], A[1][2], A[1][3], f[1].x, f[1].y);
+      if constexpr (QP == 2) mma_f16(xb, A[1][0], A[1][1], A[1][2], A[1][3], f[1].z, f[1].w);
 #pragma unroll
-      for (int i = 0; i < PAIR; ++i) qfrag(n, bl + i, f[i]);
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-        for (int i = 0; i < PAIR; ++i) {
-          if (ks == 0)
-            mma_f16_z(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i][ks].x, f[i][ks].y);
-          else
-            mma_f16(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i][ks].x, f[i][ks].y);
-        }
-        if constexpr (QP == 2) {
-#pragma unroll
-          for (int i = 0; i < PAIR; ++i)
-            mma_f16(xb[i], A[i][ks][0], A[i][ks][1], A[i][ks][2], A[i][ks][3], f[i][ks].z, f[i][ks].w);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < PAIR; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sacc[n][e] = fmaf(dkf[e >> 1][bl + i], xb[i][e], sacc[n][e]);
+      for (int e = 0; e < 4; ++e) sacc[n][e] = fmaf(dkf[e >> 1][bl], xb[e], sacc[n][e]);
     }
   };
-  uint32_t A[PAIR][2][4];
   if constexpr (KF == kKeyQ8) {
 #pragma unroll
     for (int P = 0; P < kTileBlocks / 2; ++P) {
@@ -179,15 +163,16 @@ __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QF
       const uint32_t w8[4] = {kc.x, kc.y, kc.z, kc.w};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        uint32_t A[2][4];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           // exact code -> f16: 1024 + (q + 128) - 1152
-          A[e % PAIR][ks][0] = hsub2(prmt(wg[2 * e + ks], kByte64x4, 0x4140u), kHalf2_1152);
-          A[e % PAIR][ks][2] = hsub2(prmt(wg[2 * e + ks], kByte64x4, 0x4342u), kHalf2_1152);
-          A[e % PAIR][ks][1] = hsub2(prmt(w8[2 * e + ks], kByte64x4, 0x4140u), kHalf2_1152);
-          A[e % PAIR][ks][3] = hsub2(prmt(w8[2 * e + ks], kByte64x4, 0x4342u), kHalf2_1152);
+          A[ks][0] = hsub2(prmt(wg[2 * e + ks], kByte64x4, 0x4140u), kHalf2_1152);
+          A[ks][2] = hsub2(prmt(wg[2 * e + ks], kByte64x4, 0x4342u), kHalf2_1152);
+          A[ks][1] = hsub2(prmt(w8[2 * e + ks], kByte64x4, 0x4140u), kHalf2_1152);
+          A[ks][3] = hsub2(prmt(w8[2 * e + ks], kByte64x4, 0x4342u), kHalf2_1152);
         }
-        if (e % PAIR == PAIR - 1) blocks_qk(2 * P + e - (PAIR - 1), A);
+        block_qk(2 * P + e, A);
       }
     }
   } else {
@@ -212,14 +197,15 @@ __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QF
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
+        uint32_t A[2][4];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           const uint32_t xa = wa[c] >> (8 * ks), xc = wc[c] >> (8 * ks);
           if constexpr (KF == kKeyQ4) {
-            A[c % PAIR][ks][0] = hsub2(and_or(xa, 0x000F000Fu, kHalf2Magic), kHalf2_1032);
-            A[c % PAIR][ks][2] = hfma2(and_or(xa, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kHalf2_m72);
-            A[c % PAIR][ks][1] = hsub2(and_or(xc, 0x000F000Fu, kHalf2Magic), kHalf2_1032);
-            A[c % PAIR][ks][3] = hfma2(and_or(xc, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kHalf2_m72);
+            A[ks][0] = hsub2(and_or(xa, 0x000F000Fu, kHalf2Magic), kHalf2_1032);
+            A[ks][2] = hfma2(and_or(xa, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kHalf2_m72);
+            A[ks][1] = hsub2(and_or(xc, 0x000F000Fu, kHalf2Magic), kHalf2_1032);
+            A[ks][3] = hfma2(and_or(xc, 0x00F000F0u, kHalf2Magic), kHalf2_1_16, kHalf2_m72);
           } else {
             const int slo = 4 - (4 * c + 2 * ks), shi = 7 - (4 * c + 2 * ks);
             const uint32_t ha_lo = slo >= 0 ? xa5 << slo : xa5 >> -slo;
@@ -228,15 +214,15 @@ __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QF
             const uint32_t hc_hi = shi >= 0 ? xc5 << shi : xc5 >> -shi;
             constexpr uint32_t kSubLo = KF == kKeyQ50 ? kHalf2_1040 : kHalf2Magic;
             constexpr uint32_t kAddHi = KF == kKeyQ50 ? kHalf2_m80 : kHalf2_m64;
-            A[c % PAIR][ks][0] = hsub2(or_and(and_or(xa, 0x000F000Fu, kHalf2Magic), ha_lo, 0x00100010u), kSubLo);
-            A[c % PAIR][ks][2] = hfma2(or_and(and_or(xa, 0x00F000F0u, kHalf2Magic), ha_hi, 0x01000100u), kHalf2_1_16,
+            A[ks][0] = hsub2(or_and(and_or(xa, 0x000F000Fu, kHalf2Magic), ha_lo, 0x00100010u), kSubLo);
+            A[ks][2] = hfma2(or_and(and_or(xa, 0x00F000F0u, kHalf2Magic), ha_hi, 0x01000100u), kHalf2_1_16,
                              kAddHi);
-            A[c % PAIR][ks][1] = hsub2(or_and(and_or(xc, 0x000F000Fu, kHalf2Magic), hc_lo, 0x00100010u), kSubLo);
-            A[c % PAIR][ks][3] = hfma2(or_and(and_or(xc, 0x00F000F0u, kHalf2Magic), hc_hi, 0x01000100u), kHalf2_1_16,
+            A[ks][1] = hsub2(or_and(and_or(xc, 0x000F000Fu, kHalf2Magic), hc_lo, 0x00100010u), kSubLo);
+            A[ks][3] = hfma2(or_and(and_or(xc, 0x00F000F0u, kHalf2Magic), hc_hi, 0x01000100u), kHalf2_1_16,
                              kAddHi);
           }
         }
-        if (c % PAIR == PAIR - 1) blocks_qk(4 * Q + c - (PAIR - 1), A);
+        block_qk(4 * Q + c, A);
       }
     }
   }
@@ -309,14 +295,14 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g
 //   grow         how far, in powers of two, a score may pass the running maximum (p <= 2^grow)
 //   mask(e, x)   x, or -inf where the key is unseen: token g + 8 (e / 2), row 2t + e % 2
 // The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
-template <typename L, int KF, int VF, int QP, int PP, int PAIR, typename QFrag, typename Mask>
+template <typename L, int KF, int VF, int QP, int PP, typename QFrag, typename Mask>
 __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
                                             uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], float grow,
                                             Mask mask, float (&m_run)[2], float (&l_run)[2],
                                             float (&oacc)[2 * kTileBlocks][4], float (&racc)[4]) {
   using F = TileFormat<KF, VF>;
   float sacc[1][4];
-  tile_scores<L, KF, VF, QP, 1, PAIR>(
+  tile_scores<L, KF, VF, QP, 1>(
       kb, G, g, t, [&](int, int bl, uint4 (&f)[2]) { qfrag(bl, f); }, [&](int) { return make_uint2(qsb_hi, qsb_lo); },
       sacc);
   // ---------------- online softmax (base 2) ----------------
