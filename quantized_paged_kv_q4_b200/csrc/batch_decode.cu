@@ -75,7 +75,7 @@ struct BatchUnit {
 // and either the page at hand (its first position, -1: nothing of it is fetched, and its bytes) or
 // the next step's first tile.
 struct alignas(16) Producer {
-  int unit, start, t0, n;
+  int unit, start, t0, n;  // read together, as are the next four
   int last, low, key0, next;
   const uint8_t *k, *v;
 };
@@ -489,9 +489,10 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
   // starts the copies of tile k; one group of copies per call, an empty one past the end
   auto issue = [&](int k) {
     if (k < n_tiles) {
-      int u = lds_int(&prod->unit), start = lds_int(&prod->start);
-      int end = start + lds_int(&prod->n);
-      int j = lds_int(&prod->t0) + k - start;  // the tile in the unit's list
+      const uint4 cur = lds128(smem_u32(&prod->unit));  // unit, start, t0, n
+      int u = cur.x, start = cur.y;
+      int end = start + static_cast<int>(cur.w);
+      int j = static_cast<int>(cur.z) + k - start;  // the tile in the unit's list
       if (k >= end) {
         __syncwarp();
         const BatchUnit w = next_unit(p, u);
@@ -507,8 +508,9 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
         open_page(ahead);
         if (k + 8 - G < end) ahead = page_of(p, u, (j >> 3) + 1);
       }
-      const int key0 = lds_int(&prod->key0), key = key0 + 16 * G, st = k % C::kStages;
-      const bool fetch = key0 >= 0 && key <= lds_int(&prod->last) && key + 15 >= lds_int(&prod->low);
+      const uint4 seen = lds128(smem_u32(&prod->last));  // last, low, key0
+      const int key0 = seen.z, key = key0 + 16 * G, st = k % C::kStages;
+      const bool fetch = key0 >= 0 && key <= static_cast<int>(seen.x) && key + 15 >= static_cast<int>(seen.y);
       if (lane == 0) *reinterpret_cast<volatile int*>(&key_of[st]) = fetch ? key : -1;
       if (fetch) copy_tile<KF, VF>(ring_s + st * C::kTileBytes, lds_ptr(&prod->k), lds_ptr(&prod->v), G, lane);
     }
@@ -691,14 +693,16 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
   int2 ahead = make_int2(0, -1);  // this warp's entry of the next step to be copied, loaded a step ahead
   // starts the copies of this warp's tile of the next step into stage st, and moves on
   auto issue = [&](int st) {
-    const int k0 = lds_int(&prod->next);
+    const uint4 seen = lds128(smem_u32(&prod->last));  // last, low, -, next
+    const int k0 = seen.w;
     if (k0 < n_tiles) {
-      const int u = lds_int(&prod->unit), start = lds_int(&prod->start);
-      const int end = min(start + lds_int(&prod->n), n_tiles);
+      const uint4 cur = lds128(smem_u32(&prod->unit));  // unit, start, t0, n
+      const int u = cur.x, start = cur.y;
+      const int end = min(start + static_cast<int>(cur.w), n_tiles);
       int key = -1;
       if (k0 + w < end) {
-        const int last = lds_int(&prod->last), low = lds_int(&prod->low);
-        const int G = (lds_int(&prod->t0) + k0 + w - start) & 7;
+        const int last = seen.x, low = seen.y;
+        const int G = (static_cast<int>(cur.z) + k0 + w - start) & 7;
         if (fetch_block(p, ahead, last, low, lane)) {
           key = ahead.y * kPageTokens + 16 * G;
           if (key > last || key + 15 < low) key = -1;
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       if (lane == 0) *reinterpret_cast<volatile int*>(&key_of[4 * st + w]) = key;
       // the step after it: of this unit, or the first of the next
       int next = k0 + 4, unit = u, unit_start = start, unit_end = end;
-      int t0 = lds_int(&prod->t0);
+      int t0 = cur.z;
       if (next >= end) {
         next = end;
         if (end < n_tiles) {
