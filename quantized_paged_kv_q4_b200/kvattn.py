@@ -186,11 +186,24 @@ def make_desc(n_kv_heads, n_q_heads, k_pool, v_pool, n_pages, v_fmt="q4_0", k_pa
                           n_pages, sm_budget, 0)
 
 
-def _batch_device() -> int:
-    """The current device: the batch calls launch there, and take tensors of no other."""
-    import torch
+class _Torch:
+    """What the batch calls use of torch, looked up once (an import statement and a Stream object a
+    call cost as much as the checks).  current_device: the calls launch there, and take tensors of no
+    other; raw_stream: the current stream's handle."""
 
-    return torch.cuda.current_device()
+    current_device = raw_stream = int32 = float32 = None
+    dtypes = {}
+
+
+def _torch():
+    if _Torch.current_device is None:
+        import torch
+
+        _Torch.int32, _Torch.float32 = torch.int32, torch.float32
+        _Torch.dtypes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+        _Torch.raw_stream = torch._C._cuda_getCurrentRawStream
+        _Torch.current_device = torch.cuda.current_device
+    return _Torch
 
 
 def _on(x, what, device) -> int:
@@ -204,11 +217,9 @@ def _on(x, what, device) -> int:
 
 def _i32(x, what, device, shape):
     """A device int32 array of the batch calls, or None."""
-    import torch
-
     if x is None:
         return None
-    if x.dtype is not torch.int32 or x.shape != shape:
+    if x.dtype is not _torch().int32 or x.shape != shape:
         raise ValueError(f"{what}: expected int32 {shape}, got {x.dtype} {tuple(x.shape)}")
     return _on(x, what, device)
 
@@ -221,7 +232,7 @@ def make_batch(row_start, pos_start, page_table, n_rows, max_rows) -> kvattn_bat
     if page_table.dim() != 3:
         raise ValueError(f"page_table: expected [n_seqs][H_kv][max_blocks], got {tuple(page_table.shape)}")
     n_seqs, heads, max_blocks = page_table.shape
-    device = _batch_device()
+    device = _torch().current_device()
     b = kvattn_batch(_i32(row_start, "row_start", device, (n_seqs + 1,)),
                      _i32(pos_start, "pos_start", device, (n_seqs,)),
                      _i32(page_table, "page_table", device, (n_seqs, heads, max_blocks)),
@@ -230,22 +241,15 @@ def make_batch(row_start, pos_start, page_table, n_rows, max_rows) -> kvattn_bat
     return b
 
 
-_dtypes = {}
-
-
 def make_rows(x, n_rows, heads, device=None) -> kvattn_rows:
     """A token array [n_rows][heads][256] of fp32, fp16 or bf16 as the batch calls take it: any
     strides over rows and heads (a slice of a fused projection, say), the channels contiguous."""
-    if not _dtypes:
-        import torch
-
-        _dtypes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
     at = x.get_device()
-    if at < 0 or at != (device if device is not None else _batch_device()):
+    if at < 0 or at != (device if device is not None else _torch().current_device()):
         raise ValueError(f"expected a CUDA tensor on the current device for a token array, got one on {x.device}")
     if x.shape != (n_rows, heads, 256):
         raise ValueError(f"expected a token array of shape {(n_rows, heads, 256)}, got {tuple(x.shape)}")
-    dtype = _dtypes.get(x.dtype)
+    dtype = _torch().dtypes.get(x.dtype)
     if dtype is None:
         raise ValueError(f"expected float32, float16 or bfloat16, got {x.dtype}")
     rs, hs, cs = x.stride()
@@ -256,11 +260,7 @@ def make_rows(x, n_rows, heads, device=None) -> kvattn_rows:
 
 def _batch_stream(stream, device):
     """As _s, with the current stream's handle taken directly (the Stream object costs 4 us a call)."""
-    if stream is None:
-        import torch
-
-        return torch._C._cuda_getCurrentRawStream(device)
-    return _s(stream)
+    return _torch().raw_stream(device) if stream is None else _s(stream)
 
 
 # ---------------------------------------------------------------- entry points
@@ -410,9 +410,9 @@ def _check_batch(what, desc, batch) -> int:
     """The device of a batch call: the batch's, which has to be the current one."""
     if batch.heads != desc.n_kv_heads:
         raise ValueError(f"{what}: page_table has {batch.heads} KV heads, the descriptor {desc.n_kv_heads}")
-    device = batch.device
-    if device != _batch_device():
-        raise ValueError(f"{what}: the batch is on cuda:{device}, the current device is cuda:{_batch_device()}")
+    device, now = batch.device, _torch().current_device()
+    if device != now:
+        raise ValueError(f"{what}: the batch is on cuda:{device}, the current device is cuda:{now}")
     return device
 
 
@@ -442,11 +442,9 @@ def kvattn_decode_batch_workspace_size(desc, batch) -> int:
 def kvattn_decode_batch(desc, batch, q, out, lse, ws, page_logical=None, n_pages=None, window=0, stream=None) -> None:
     """Attention of every row of the batch over its sequence's pages: q, out [n_rows][H_q][256] of one
     type, lse fp32 [n_rows][H_q], ws a tensor of at least kvattn_decode_batch_workspace_size bytes."""
-    import torch
-
     device = _check_batch("kvattn_decode_batch", desc, batch)
     n, heads, q_heads = batch.n_rows, batch.heads, desc.n_q_heads
-    if lse.dtype is not torch.float32 or lse.shape != (n, q_heads):
+    if lse.dtype is not _torch().float32 or lse.shape != (n, q_heads):
         raise ValueError(f"lse: expected float32 {(n, q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
     _check(lib().kvattn_decode_batch(desc, batch, make_rows(q, n, q_heads, device),
                                      _i32(page_logical, "page_logical", device, (batch.n_seqs, heads, batch.max_blocks)),
