@@ -150,8 +150,9 @@ struct WideCfg {
   static_assert(kGroups >= 1 && kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
   static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
   // 48 windowed sequences in 38.2, 35.6 and 37.8 us with (3, 4), (6, 8) and (10, 16), eight verify
-  // steps in 65.5, 63.5 and 62.2
-  static constexpr int kUnitCost = 6, kMinShare = 8;
+  // steps in 65.5, 63.5 and 62.2.  With 7 a unit of one tile fills a share: 16 sequences of one to
+  // four tokens in 14.5 us, with 8 (two units in some groups) in 21.2
+  static constexpr int kUnitCost = 6, kMinShare = 7;
 };
 
 __device__ __forceinline__ int lds_int(const int* p) { return static_cast<int>(lds32(smem_u32(p))); }
