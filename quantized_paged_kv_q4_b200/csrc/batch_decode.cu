@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
   // makes entry `e` the page at hand
   auto open_page = [&](int2 e) {
     const bool fetch = fetch_block(p, e, lds_int(&prod->last), lds_int(&prod->low), lane);
+    __syncwarp();  // every lane has read the page before (the ring is filled without a barrier between tiles)
     if (lane == 0) {
       prod->key0 = fetch ? e.y * kPageTokens : -1;
       prod->k = p.b.k_pool + e.x * p.b.k_stride;  // used only when fetched
