@@ -500,7 +500,7 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
  * 2^-9 of the output's rounding.
  * Supports group * max_rows <= 24 and n_seqs * H_kv * max_blocks <= 2^27 (table entries).
  * Results do not depend on timing: the split of the work depends on the lengths and the device
- * alone. */
+ * alone.  The workspace size is 0 for a batch that kvattn_decode_batch refuses. */
 KVATTN_API size_t kvattn_decode_batch_workspace_size(const kvattn_kv_desc* desc, const kvattn_batch* batch);
 KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batch* batch, const kvattn_rows* q,
                                    const int32_t* page_logical, const int32_t* n_pages, int32_t window,

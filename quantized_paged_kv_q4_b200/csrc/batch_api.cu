@@ -64,6 +64,18 @@ BatchParams params_of(const kvattn_kv_desc* d, const kvattn_batch* b) {
   return p;
 }
 
+long long most_tiles_of(const kvattn_kv_desc* d, const kvattn_batch* b) {
+  return static_cast<long long>(b->n_seqs) * d->n_kv_heads * 8 * std::max(b->max_blocks, 1);
+}
+
+// What a decode supports beyond validate_batch: query rows of a unit that the kernels hold ...
+bool decode_rows_ok(const kvattn_kv_desc* d, const kvattn_batch* b) {
+  return static_cast<int64_t>(d->n_q_heads / d->n_kv_heads) * b->max_rows <= 24;
+}
+
+// ... and a line of all units' tiles (and a few per unit beside them) that is counted in 32 bits.
+bool decode_tiles_ok(const kvattn_kv_desc* d, const kvattn_batch* b) { return most_tiles_of(d, b) <= (1ll << 30); }
+
 // The workspace of a decode: where every unit's partials are, and two partials per group.
 struct BatchPlan {
   int sms;
@@ -75,7 +87,7 @@ BatchPlan plan_batch(const kvattn_kv_desc* d, const kvattn_batch* b) {
   BatchPlan p{};
   p.sms = sm_budget_of(d);
   const long long units = static_cast<long long>(b->n_seqs) * d->n_kv_heads;
-  p.most_tiles = units * 8 * std::max(b->max_blocks, 1);
+  p.most_tiles = most_tiles_of(d, b);
   const int row_tiles = batch_row_tiles(d->n_q_heads / d->n_kv_heads * std::max(b->max_rows, 1));
   const size_t slots = static_cast<size_t>(batch_group_bound(p.sms, row_tiles)) * 2 * row_tiles * 8;
   p.lse_off = round_up(sizeof(int2) * std::max(units, 1ll), 256);
@@ -135,7 +147,7 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
 }
 
 KVATTN_API size_t kvattn_decode_batch_workspace_size(const kvattn_kv_desc* desc, const kvattn_batch* batch) {
-  if (validate_batch(desc, batch)) return 0;
+  if (validate_batch(desc, batch) || !decode_rows_ok(desc, batch) || !decode_tiles_ok(desc, batch)) return 0;
   return plan_batch(desc, batch).bytes;
 }
 
@@ -147,16 +159,14 @@ KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batc
   int st = validate_batch(desc, batch);
   if (st) return st;
   if (window < 0) return KVATTN_ERR_INVALID_ARG;
-  const int group = desc->n_q_heads / desc->n_kv_heads;
-  if (static_cast<int64_t>(group) * batch->max_rows > 24) return KVATTN_ERR_UNSUPPORTED_SHAPE;
+  if (!decode_rows_ok(desc, batch)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
   if (nothing_to_do(batch)) return KVATTN_OK;
   if ((st = validate_rows(q, batch->n_rows, desc->n_q_heads, false))) return st;
   if ((st = validate_rows(out, batch->n_rows, desc->n_q_heads, true))) return st;
   if (q->dtype != out->dtype) return KVATTN_ERR_UNSUPPORTED_FORMAT;
   if (!lse) return KVATTN_ERR_INVALID_ARG;
+  if (!decode_tiles_ok(desc, batch)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
   const BatchPlan plan = plan_batch(desc, batch);
-  // the line of all units' tiles (and a few per unit beside them) is counted in 32 bits
-  if (plan.most_tiles > (1ll << 30)) return KVATTN_ERR_UNSUPPORTED_SHAPE;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return KVATTN_ERR_INVALID_ARG;
   if (ws_bytes < plan.bytes) return KVATTN_ERR_WORKSPACE_TOO_SMALL;
   int dev;
@@ -168,7 +178,7 @@ KVATTN_API int kvattn_decode_batch(const kvattn_kv_desc* desc, const kvattn_batc
   p.lse = lse;
   p.page_logical = page_logical;
   p.n_list = n_pages;
-  p.group = group;
+  p.group = desc->n_q_heads / desc->n_kv_heads;
   p.window = window;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.unit_parts = reinterpret_cast<int2*>(w);
