@@ -36,7 +36,8 @@ template <int HALF>
 __device__ __forceinline__ int offset_code(float x, float inv) {
   const float y = __fmul_rn(x, inv);
   const float z = __fadd_rn(y, HALF + 0.5f);
-  return min(2 * HALF - 1, __float2int_rz(z));  // z > 0, so truncation is floor
+  // z > 0, so truncation is floor; where 1 / d overflowed it may be anything, and still ends as a code
+  return min(2 * HALF - 1, max(0, __float2int_rz(z)));
 }
 __device__ __forceinline__ int q4_code(float x, float inv) { return offset_code<8>(x, inv); }
 
