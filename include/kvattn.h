@@ -495,9 +495,7 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
  *                out = 0)
  *   ws           device workspace of kvattn_decode_batch_workspace_size() bytes, 256-byte
  *                aligned; needs no initialisation.  Calls that share one must not overlap.
- * Accuracy: fp32 and fp16 as kvattn_decode (about 2^-20 relative before fp16's own rounding).  With
- * bf16, P and P x the value's scale are rounded to f16 (2^-12 each, of what is summed) before the
- * 2^-9 of the output's rounding.
+ * Accuracy: as kvattn_decode (about 2^-20 relative) before the output's own rounding.
  * Supports group * max_rows <= 24 and n_seqs * H_kv * max_blocks <= 2^27 (table entries).
  * Results do not depend on timing: the split of the work depends on the lengths and the device
  * alone.  The workspace size is 0 for a batch that kvattn_decode_batch refuses. */

@@ -57,12 +57,10 @@ struct BatchDecodeParams {
 };
 
 // 16-bit inputs are exact as one f16 part (bf16's 8 bits after scaling by a power of two); fp32
-// queries take two.  P keeps two parts unless the output is bf16: one rounding of P and one of
-// P x scale to f16 (2^-12 each) are an eighth of the rounding of the store (2^-9).
+// queries take two.
 template <typename T>
 struct BatchParts {
   static constexpr int kQ = sizeof(T) == 4 ? 2 : 1;
-  static constexpr int kP = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;
 };
 
 // One unit: its n tiles start at tile t0 of its list of pages (n = 0: a sequence without rows).
@@ -133,7 +131,7 @@ struct WideCfg {
   using L = SingleTileLayout<KF, VF>;
   static constexpr int kRowsPad = 8 * NR;
   static constexpr int kTileBytes = L::kBytes;
-  static constexpr int kPFragBytes = BatchParts<T>::kP == 2 ? 16 : 8;
+  static constexpr int kPFragBytes = 16;
   static constexpr int kQTileBytes = BatchParts<T>::kQ * 8 * 32 * 16;  // of one n-tile
   static constexpr int kPTileBytes = NR * 32 * kPFragBytes;   // of one tile of tokens
   static constexpr int kFixed = NR * kQTileBytes + 4 * kPTileBytes + sizeof(WideState<NR>);
@@ -455,7 +453,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
   using C = BatchCfg<KF, VF, T>;
   using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
-  constexpr int QP = BatchParts<T>::kQ, PP = BatchParts<T>::kP;
+  constexpr int QP = BatchParts<T>::kQ;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -578,7 +576,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
-        attend_tile<L, KF, VF, QP, PP>(
+        attend_tile<L, KF, VF, QP>(
             kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow, 2.f,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
@@ -669,7 +667,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
   using C = WideCfg<KF, VF, NR, T>;
   using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
-  constexpr int QP = BatchParts<T>::kQ, PP = BatchParts<T>::kP;
+  constexpr int QP = BatchParts<T>::kQ;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -890,18 +888,10 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           l_run[n][c] += pr[c] + pr[c + 2];
         }
         const uint32_t to = p_s + w * C::kPTileBytes + (n * 32 + lane) * C::kPFragBytes;
-        if constexpr (PP == 2) {
-          uint32_t h01, l01, h23, l23;
-          split_pair(pr[0], pr[1], h01, l01);
-          split_pair(pr[2], pr[3], h23, l23);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(movmatrix_t(h01)),
-                       "r"(movmatrix_t(h23)), "r"(movmatrix_t(l01)), "r"(movmatrix_t(l23))
-                       : "memory");
-        } else {
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(movmatrix_t(pack_half2(pr[0], pr[1]))),
-                       "r"(movmatrix_t(pack_half2(pr[2], pr[3])))
-                       : "memory");
-        }
+        uint32_t h01, l01, h23, l23;
+        split_pair(pr[0], pr[1], h01, l01);
+        split_pair(pr[2], pr[3], h23, l23);
+        sts128(to, movmatrix_t(h01), movmatrix_t(h23), movmatrix_t(l01), movmatrix_t(l23));
       }
       group_sync();
       // ---- O^T += V^T P^T for this warp's channels, over the step's tiles
@@ -910,14 +900,8 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
         uint32_t ph[NR][2], pl[NR][2];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-          const uint32_t from = p_s + u * C::kPTileBytes + (n * 32 + lane) * C::kPFragBytes;
-          if constexpr (PP == 2) {
-            const uint4 v = lds128(from);
-            ph[n][0] = v.x, ph[n][1] = v.y, pl[n][0] = v.z, pl[n][1] = v.w;
-          } else {
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(ph[n][0]), "=r"(ph[n][1]) : "r"(from));
-            pl[n][0] = pl[n][1] = 0u;
-          }
+          const uint4 v = lds128(p_s + u * C::kPTileBytes + (n * 32 + lane) * C::kPFragBytes);
+          ph[n][0] = v.x, ph[n][1] = v.y, pl[n][0] = v.z, pl[n][1] = v.w;
         }
         int e = 0;  // constant in the unrolled code
         tile_value_pair<L, KF, VF>(
@@ -925,12 +909,12 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
                 uint32_t bh0, bl0, bh1, bl1;
-                scale_p<PP>(ph[n][0], pl[n][0], d0, bh0, bl0);
-                scale_p<PP>(ph[n][1], pl[n][1], d1, bh1, bl1);
+                split_scaled(ph[n][0], pl[n][0], d0, bh0, bl0);
+                split_scaled(ph[n][1], pl[n][1], d1, bh1, bl1);
                 mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
-                if constexpr (PP == 2) mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
+                mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
                 mma_f16(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
-                if constexpr (PP == 2) mma_f16(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
+                mma_f16(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
               }
               ++e;
             });
@@ -942,7 +926,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
             mma_f16(racc[n], m01, 0u, m89, 0u, ph[n][0], ph[n][1]);
-            if constexpr (PP == 2) mma_f16(racc[n], m01, 0u, m89, 0u, pl[n][0], pl[n][1]);
+            mma_f16(racc[n], m01, 0u, m89, 0u, pl[n][0], pl[n][1]);
           }
         }
       };

@@ -66,17 +66,6 @@ __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uin
   lo = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
 }
 
-// P (its f16 parts) times the per-token scales f of a block: PP parts of the product.
-template <int PP>
-__device__ __forceinline__ void scale_p(uint32_t ph, uint32_t pl, uint32_t f, uint32_t& hi, uint32_t& lo) {
-  if constexpr (PP == 2) {
-    split_scaled(ph, pl, f, hi, lo);
-  } else {
-    hi = hmul2(ph, f);
-    lo = 0u;
-  }
-}
-
 // Where the parts of a page sit in a shared-memory copy: a whole page (tile G of it is read) ...
 template <int KF, int VF>
 struct PageLayout {
@@ -288,14 +277,14 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g
 
 // Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
 // lane % 4; the thread's rows are 2t, 2t + 1).
-//   QP, PP       f16 parts of the query and of P: 2 keeps about 22 bits of each, 1 rounds once
+//   QP           f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
 //   qfrag(b, f)  fills f[k-step] with the query's B fragments of block b (hi0, hi1, lo0, lo1)
 //   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment
 //   crow         turns a dot product with the normalised row into a base-2 softmax score
 //   grow         how far, in powers of two, a score may pass the running maximum (p <= 2^grow)
 //   mask(e, x)   x, or -inf where the key is unseen: token g + 8 (e / 2), row 2t + e % 2
 // The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
-template <typename L, int KF, int VF, int QP, int PP, typename QFrag, typename Mask>
+template <typename L, int KF, int VF, int QP, typename QFrag, typename Mask>
 __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
                                             uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], float grow,
                                             Mask mask, float (&m_run)[2], float (&l_run)[2],
@@ -342,7 +331,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
     }
   }
   // P as f16 parts, transposed in registers into B fragments
-  uint32_t pbh[2], pbl[2] = {0u, 0u};
+  uint32_t pbh[2], pbl[2];
   {
     float pr[4];
 #pragma unroll
@@ -352,33 +341,28 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
       pr[c + 2] = fast_exp2(sv[c + 2] - mu);
       l_run[c] += pr[c] + pr[c + 2];
     }
-    if constexpr (PP == 2) {
-      uint32_t h01, l01, h23, l23;
-      split_pair(pr[0], pr[1], h01, l01);
-      split_pair(pr[2], pr[3], h23, l23);
-      pbh[0] = movmatrix_t(h01);
-      pbh[1] = movmatrix_t(h23);
-      pbl[0] = movmatrix_t(l01);
-      pbl[1] = movmatrix_t(l23);
-    } else {
-      pbh[0] = movmatrix_t(pack_half2(pr[0], pr[1]));
-      pbh[1] = movmatrix_t(pack_half2(pr[2], pr[3]));
-    }
+    uint32_t h01, l01, h23, l23;
+    split_pair(pr[0], pr[1], h01, l01);
+    split_pair(pr[2], pr[3], h23, l23);
+    pbh[0] = movmatrix_t(h01);
+    pbh[1] = movmatrix_t(h23);
+    pbl[0] = movmatrix_t(l01);
+    pbl[1] = movmatrix_t(l23);
   }
   // ---------------- O^T += V^T P^T ----------------
-  // V codes enter the MMA exactly; the per-token block scale multiplies P (in PP f16
-  // parts), PP MMAs per 16-dimension half.
+  // V codes enter the MMA exactly; the per-token block scale multiplies P (in two f16
+  // parts), two MMAs per 16-dimension half.
 #pragma unroll
   for (int C = 0; C < kTileBlocks / 2; ++C)
     tile_value_pair<L, KF, VF>(vb, G, C, g, t,
                                [&](int bl, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
       uint32_t bh0, bl0, bh1, bl1;
-      scale_p<PP>(pbh[0], pbl[0], d0, bh0, bl0);
-      scale_p<PP>(pbh[1], pbl[1], d1, bh1, bl1);
+      split_scaled(pbh[0], pbl[0], d0, bh0, bl0);
+      split_scaled(pbh[1], pbl[1], d1, bh1, bl1);
       mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
-      if constexpr (PP == 2) mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
+      mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
       mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
-      if constexpr (PP == 2) mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
+      mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
     });
   if constexpr (F::kVMin) {
     // sum over the tile's tokens of p * m for all 8 blocks at once: A = the minima
@@ -389,7 +373,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
                  : "=r"(m01), "=r"(m89)
                  : "r"(vb + L::kVMinimum + (((G * 4 + t) * 8 + g) * 4) * 2));
     mma_f16(racc, m01, 0u, m89, 0u, pbh[0], pbh[1]);
-    if constexpr (PP == 2) mma_f16(racc, m01, 0u, m89, 0u, pbl[0], pbl[1]);
+    mma_f16(racc, m01, 0u, m89, 0u, pbl[0], pbl[1]);
   }
 }
 

@@ -12,6 +12,142 @@ pytestmark = pytest.mark.gpu
 TYPES = ["float32", "float16", "bfloat16"]
 
 
+# --------------------------------------------------- what the header states, with no floor of its own
+def exact_rows(q, k, v):
+    """Attention of rows q [n][256] over keys k and values v [T][256], float64, with what the bound needs:
+    (o, lse, p [n][T], sum_c |q k| / 16 at its largest, [n])."""
+    q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
+    s = q @ k.T / 16.0
+    m = s.max(1, keepdims=True)
+    p = np.exp(s - m)
+    tot = p.sum(1, keepdims=True)
+    big = np.array([(np.abs(a) @ np.abs(k).T).max() for a in q]) / 16.0
+    return p / tot @ v, (m + np.log(tot))[:, 0], p / tot, big
+
+
+def half_step(x, dtype):
+    least = {"float32": -126, "float16": -14, "bfloat16": -126}[dtype]
+    return np.exp2(np.maximum(np.floor(np.log2(np.maximum(x, 1e-300))), least)) * EPS[dtype]
+
+
+def check_range(out, lse, ref, v, codes, scales, dtype, tiles):
+    """The bounds of the header, by arithmetic.
+    Scores: products of a query held to 22 bits (fp32; 16-bit queries are exact here), accumulated in fp32
+    by 4 MMAs in each of 8 blocks: 2^-18 of sum |q k| / 16 = big, and 2^-21 for the exponential, in the
+    numerator and in the sum.
+    P and P x scale: 2^-22 each in two f16 parts; the parts end 2^-37 below the row's largest P times the larger
+    of 1 and the largest scale (P), and 2^-36 below the largest P times the largest scale (the product).
+    Accumulation: one step per MMA, two MMAs per tile of 16 keys, in a group's share of `tiles`: each
+    step cuts at most 2^-23 of the sum so far, twice what a rounding would; a merge adds a few.
+    (fp32 outputs add every tile's two MMAs by themselves: within the same bound.)
+    The store rounds once, by half a step of the value's own binade."""
+    o_ref, lse_ref, p, big = ref
+    dmax = float(np.abs(scales).max())
+    top = p.max(1, keepdims=True)
+    mass = np.abs(v) + codes * scales  # what is added: codes times scales, and minima
+    pv = p @ mass
+    floor = top * (2.0 ** -37 * max(1.0, dmax) * mass.sum(0) + 2.0 ** -36 * max(dmax, 2.0 ** -16) * codes.sum(0))
+    ew = 2.0 ** -18 * big + 2.0 ** -21
+    tol = (2 * ew + 2.0 ** -20 + (2 * tiles + 64) * 2.0 ** -23)[:, None] * pv + floor
+    tol = tol + half_step(np.abs(o_ref) + tol, dtype)
+    gone = ~np.isfinite(lse_ref)  # rows that see a key which fp16 does not hold
+    assert not np.isfinite(out[gone]).any() and not np.isfinite(lse[gone]).any()
+    if gone.any():
+        return tol
+    err = np.abs(np.asarray(out, np.float64) - o_ref)
+    worst = np.unravel_index(np.argmax(err / tol), err.shape)
+    assert (err <= tol).all(), (worst, err[worst], tol[worst], o_ref[worst])
+    ltol = ew + (2 * tiles + 64) * 2.0 ** -23 + np.abs(lse_ref) * 2.0 ** -22
+    assert (np.abs(lse - lse_ref) <= ltol).all(), np.abs(lse - lse_ref).max()
+    return tol
+
+
+class History:
+    """One KV head's T tokens in oracle-encoded pages, which any number of sequences share."""
+
+    def __init__(self, kv, group, k_fmt, v_fmt, k, v, poison=()):
+        """poison: (token, block, 0 or 1 for the value's scale or minimum, what to put there)."""
+        import torch
+
+        T = k.shape[0]
+        self.T, self.group, self.v_fmt, n = T, group, v_fmt, (T + 127) // 128
+        pools, self.held, quantized = [], [], []
+        for role, fmt, x in (("k", k_fmt, k), ("v", v_fmt, v)):
+            codes, d = oq.quantize(x, fmt)
+            if role == "v":
+                for token, block, which, what in poison:
+                    d[(token, block) + ((which,) if d.ndim == 3 else ())] = what
+            quantized.append((codes, d))
+            self.held.append(oq.dequantize(codes, d, fmt))
+            pad = lambda a: np.concatenate([a, np.zeros((n * 128 - T,) + a.shape[1:], a.dtype)])  # noqa: E731
+            codes, d = pad(codes), pad(d)
+            pages = [np.asarray(olay.encode_page(role, fmt, codes[128 * b:128 * b + 128], d[128 * b:128 * b + 128]))
+                     .view(np.uint8).reshape(-1) for b in range(n)]
+            pools.append(torch.from_numpy(np.stack(pages)).cuda())
+        codes, d = quantized[1]
+        d = np.abs((d if d.ndim == 2 else d[..., 0]).astype(np.float64))
+        self.codes = np.abs(codes.astype(np.int64) - (8 if v_fmt == "q4_0" else 0)).reshape(-1, 256)
+        self.scales = np.repeat(d, 32, axis=-1)
+        self.pools, self.n = pools, n
+        self.table = torch.arange(n, dtype=torch.int32, device="cuda")[None, None]
+        self.desc = kv.make_desc(1, group, *pools, n, k_fmt=k_fmt, v_fmt=v_fmt)
+
+    def exact(self, q):
+        return exact_rows(q, *self.held)
+
+    def check(self, out, lse, ref, dtype):
+        return check_range(out, lse, ref, self.held[1], self.codes, self.scales, dtype, self.n * 8)
+
+    def decode(self, kv, name, n_seqs, budget, q):
+        """The newest token of n_seqs sequences, queries q [1][group][256] each, on `budget` SMs."""
+        return self.batch(kv, name, np.repeat(q, n_seqs, 0), [self.T - 1] * n_seqs, [1] * n_seqs, budget=budget)
+
+    def batch(self, kv, name, q, pos, rows, window=0, budget=0, listed=False):
+        """Sequences of rows[s] tokens from position pos[s] on, queries q [sum of rows][group][256]."""
+        import torch
+
+        self.desc.sm_budget = budget
+        S = len(pos)
+        row = torch.from_numpy(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)).cuda()
+        start = torch.tensor(pos, dtype=torch.int32, device="cuda")
+        table = self.table.expand(S, 1, self.n).contiguous()
+        batch = kv.make_batch(row, start, table, int(sum(rows)), max(rows))
+        qt = torch.from_numpy(np.ascontiguousarray(q)).to(getattr(torch, name)).cuda()
+        out, lse = torch.zeros_like(qt), torch.zeros(qt.shape[:2], device="cuda")
+        ws = torch.empty(kv.kvattn_decode_batch_workspace_size(self.desc, batch), dtype=torch.uint8, device="cuda")
+        kw = {"page_logical": table, "n_pages": torch.full((S, 1), self.n, dtype=torch.int32, device="cuda")} if listed else {}
+        kv.kvattn_decode_batch(self.desc, batch, qt, out, lse, ws, window=window, **kw)
+        assert kv.kvattn_device_error() == 0
+        return out.float().cpu().numpy(), lse.cpu().numpy()
+
+
+def history(rng, T, spread, mean, logit, q_scale, group):
+    """Keys and queries with N(0, q_scale) scores, key 0 `logit` above them with a value near zero."""
+    sign = np.where(rng.random(256) < 0.5, -1.0, 1.0).astype(np.float32)
+    k = rng.standard_normal((T, 256)).astype(np.float32)
+    v = (rng.standard_normal((T, 256)) * spread + mean).astype(np.float32)
+    q = (rng.standard_normal((1, group, 256)) * q_scale).astype(np.float32)
+    if logit:
+        k[0] = sign
+        v[0] *= 1e-3
+        q = q + (logit / 16 - q @ sign / 256)[..., None] * sign  # q . k0 / 16 = logit
+    return k, v, q.astype(np.float32)
+
+
+@pytest.mark.parametrize("name", ["float16", "bfloat16"])
+@pytest.mark.parametrize("group", [6, 20])
+def test_outputs_of_16_bits_are_rounded_once(kv_gpu, name, group):
+    """What the kernel holds before the store is as exact as for fp32: the output is the definition's nearest
+    value, but where that lies within the header's bound of a border between two."""
+    for k_fmt, v_fmt in PAIRS:
+        k, v, q = history(np.random.default_rng(15), 700, 1.0, 0.1, 0, 1.0, group)
+        c = History(kv_gpu, group, k_fmt, v_fmt, k, v)
+        qx = rounded(q, name)[0]
+        out, lse = c.decode(kv_gpu, name, 3, 1, qx)
+        for s in range(3):
+            c.check(out[s], lse[s], c.exact(qx[0]), name)
+
+
 # ------------------------------------------------------------- the shares of the work
 @pytest.mark.parametrize("name", ["float32", "bfloat16"])
 def test_ring_fills_over_a_pages_end(kv_gpu, name):
