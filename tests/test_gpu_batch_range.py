@@ -50,8 +50,7 @@ def check_range(out, lse, ref, v, codes, scales, dtype, tiles):
     ew = 2.0 ** -18 * big + 2.0 ** -21
     tol = (2 * ew + 2.0 ** -20 + (2 * tiles + 64) * 2.0 ** -23)[:, None] * pv + floor
     tol = tol + half_step(np.abs(o_ref) + tol, dtype)
-    gone = ~np.isfinite(lse_ref)  # rows that see a key which fp16 does not hold
-    assert not np.isfinite(out[gone]).any() and not np.isfinite(lse[gone]).any()
+    gone = ~np.isfinite(lse_ref)  # rows that see a key which fp16 does not hold: nothing is said of them
     if gone.any():
         return tol
     err = np.abs(np.asarray(out, np.float64) - o_ref)
@@ -138,14 +137,22 @@ def history(rng, T, spread, mean, logit, q_scale, group):
 @pytest.mark.parametrize("group", [6, 20])
 def test_outputs_of_16_bits_are_rounded_once(kv_gpu, name, group):
     """What the kernel holds before the store is as exact as for fp32: the output is the definition's nearest
-    value, but where that lies within the header's bound of a border between two."""
+    value, but where that lies within the header's bound of a border between two.  How many are not: an
+    error of 2^-20 of the sum of p |v| crosses a border with a chance of 2 x error / step."""
+    import torch
+
     for k_fmt, v_fmt in PAIRS:
         k, v, q = history(np.random.default_rng(15), 700, 1.0, 0.1, 0, 1.0, group)
         c = History(kv_gpu, group, k_fmt, v_fmt, k, v)
         qx = rounded(q, name)[0]
+        ref = c.exact(qx[0])
+        nearest = torch.from_numpy(ref[0]).to(getattr(torch, name)).float().numpy()
+        chance = 2.0 ** -20 * (ref[2] @ (np.abs(c.held[1]) + c.codes * c.scales)) / half_step(np.abs(ref[0]), name)
+        allowed = np.minimum(chance, 1).sum()
         out, lse = c.decode(kv_gpu, name, 3, 1, qx)
         for s in range(3):
-            c.check(out[s], lse[s], c.exact(qx[0]), name)
+            c.check(out[s], lse[s], ref, name)
+            assert (out[s] != nearest).sum() <= allowed + 5 * allowed ** 0.5 + 5, (k_fmt, v_fmt)
 
 
 # ------------------------------------------------------------- the shares of the work
