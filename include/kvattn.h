@@ -495,7 +495,9 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
  *                out = 0)
  *   ws           device workspace of kvattn_decode_batch_workspace_size() bytes, 256-byte
  *                aligned; needs no initialisation.  Calls that share one must not overlap.
- * Accuracy: as kvattn_decode (about 2^-20 relative) before the output's own rounding.
+ * Accuracy: as kvattn_decode (about 2^-20 relative) before the output's own rounding.  Queries: fp16 rows
+ * and bf16 elements within 2^-32 of their row's largest are exact, fp32 elements within 2^-17 of it keep 22
+ * bits; smaller ones are held to 2^-39 of the largest.
  * Supports group * max_rows <= 24 and n_seqs * H_kv * max_blocks <= 2^27 (table entries).
  * Results do not depend on timing: the split of the work depends on the lengths and the device
  * alone.  The workspace size is 0 for a batch that kvattn_decode_batch refuses. */

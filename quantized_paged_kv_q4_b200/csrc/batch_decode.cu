@@ -56,11 +56,14 @@ struct BatchDecodeParams {
   float* part_o;    // [groups][2][rows_pad][256]
 };
 
-// 16-bit inputs are exact as one f16 part (bf16's 8 bits after scaling by a power of two); fp32
-// queries take two.
+// The query's f16 parts, and the power of two that its row's largest magnitude is scaled to (2^kTop to 2^(kTop
+// + 1), as high as f16 holds it: elements far below it keep their bits).  16-bit inputs take one part: every
+// fp16 row is exact so, and a bf16 element down to 2^-32 of the row's largest (below that, to 2^-40 of it).
+// fp32 takes two, about 22 bits down to 2^-17 of the largest, and 2^-39 of it below.
 template <typename T>
 struct BatchParts {
-  static constexpr int kQ = sizeof(T) == 4 ? 2 : 1;
+  static constexpr int kQ = sizeof(T) == 4 ? 2 : 1, kTop = sizeof(T) == 4 ? 14 : 15;
+  static constexpr int kSum = 6;  // block sums (zero-point keys) are 2^5 elements: divided by 2^6 they fit f16
 };
 
 // One unit: its n tiles start at tile t0 of its list of pages (n = 0: a sequence without rows).
@@ -324,7 +327,7 @@ __device__ __forceinline__ void load_qfrag(uint32_t q_s, int bl, int lane, uint4
 }
 
 // The B fragments of query rows 8 nt .. + 7 of the unit, to shared memory (one warp).  A row is scaled by
-// the power of two that puts its largest magnitude into [1, 2) (exact), and split into f16 parts.
+// the power of two that puts its largest magnitude into [2^kTop, 2^(kTop + 1)), and split into f16 parts.
 // Returns what turns a dot product with scaled row g into a base-2 score; zero-point keys: the
 // rows' block sums as a B fragment.  `between` runs while the rows are on their way.
 template <typename T, int QP, bool KMIN, typename Between>
@@ -358,9 +361,10 @@ __device__ __forceinline__ float query_fragments(const BatchDecodeParams& p, con
     for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[b][e]));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  // 2^e <= amax < 2^(e+1), kept where both 2^e and 2^-e are normal numbers
-  const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 1), 253);
-  const float inv = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+  // 2^e <= amax < 2^(e+1), kept where both 2^(e - kTop) and 2^(kTop - e) are normal numbers
+  constexpr int kTop = BatchParts<T>::kTop;
+  const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23), kTop + 1), 254);
+  const float inv = __uint_as_float(static_cast<uint32_t>(254 + kTop - ex) << 23);
   float qs0 = 0.f, qs1 = 0.f;
 #pragma unroll
   for (int bl = 0; bl < kBlocks; ++bl) {
@@ -384,14 +388,19 @@ __device__ __forceinline__ float query_fragments(const BatchDecodeParams& p, con
       float sm = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sm += xv[e];
+      sm *= 1.f / (1 << BatchParts<T>::kSum);
       sm += __shfl_xor_sync(0xffffffffu, sm, 1);
       sm += __shfl_xor_sync(0xffffffffu, sm, 2);
       if (bl == 2 * t) qs0 = sm;
       if (bl == 2 * t + 1) qs1 = sm;
     }
   }
-  if constexpr (KMIN) split_pair(qs0, qs1, qsb_hi, qsb_lo);
-  return __uint_as_float(static_cast<uint32_t>(ex) << 23) * (1.0f / 16.0f) * 1.4426950408889634f;
+  if constexpr (KMIN) {
+    // the remainders are 2^11 below at least: as much higher they fit f16 too
+    qsb_hi = pack_half2(qs0, qs1);
+    qsb_lo = pack_half2((qs0 - half_lo(qsb_hi)) * 2048.f, (qs1 - half_hi(qsb_hi)) * 2048.f);
+  }
+  return __uint_as_float(static_cast<uint32_t>(ex - kTop) << 23) * (1.0f / 16.0f) * 1.4426950408889634f;
 }
 
 // Entry i of unit u's list: page and logical block (-1: no such entry).
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
   using C = BatchCfg<KF, VF, T>;
   using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
-  constexpr int QP = BatchParts<T>::kQ;
+  constexpr int QP = BatchParts<T>::kQ, QSUM = BatchParts<T>::kSum;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
-        attend_tile<L, KF, VF, QP>(
+        attend_tile<L, KF, VF, QP, QSUM>(
             kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow, 2.f,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
@@ -667,7 +676,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
   using C = WideCfg<KF, VF, NR, T>;
   using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
-  constexpr int QP = BatchParts<T>::kQ;
+  constexpr int QP = BatchParts<T>::kQ, QSUM = BatchParts<T>::kSum;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -804,7 +813,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           uint8_t* vs = ring + st * C::kStepBytes + w * C::kTileBytes + L::kV + L::kVScale;
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
-        tile_scores<L, KF, VF, QP, NR>(
+        tile_scores<L, KF, VF, QP, QSUM, NR>(
             kb, 0, g, t,
             [&](int n, int bl, uint4 (&f)[2]) { load_qfrag<QP>(q_s + n * C::kQTileBytes, bl, lane, f); },
             [&](int n) { return state->qsums[n][lane]; }, sv);

@@ -93,10 +93,11 @@ struct SingleTileLayout {
 // 4): sacc[n][e] is token g + 8 (e / 2), row 2t + e % 2 of n-tile n.
 //   QP             f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
 //   qfrag(n, b, f) fills f[k-step] with the B fragments of n-tile n, block b (hi0, hi1, lo0, lo1)
-//   qsums(n)       zero-point keys: the query's block sums as a B fragment (hi, lo)
+//   qsums(n)       zero-point keys: the query's block sums as a B fragment (hi, lo); with QSUM > 0 divided by
+//                  2^QSUM, and lo times 2^11
 // (Interleaving the MMAs of two blocks measured no faster in any kernel, for 12 more registers.)
 // The tile is tile G of the copy at kb, arranged as L.
-template <typename L, int KF, int VF, int QP, int NR, typename QFrag, typename QSums>
+template <typename L, int KF, int VF, int QP, int QSUM, int NR, typename QFrag, typename QSums>
 __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QFrag qfrag, QSums qsums,
                                             float (&sacc)[NR][4]) {
   using F = TileFormat<KF, VF>;
@@ -222,8 +223,17 @@ __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QF
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       const uint2 qs = qsums(n);
-      mma_f16(sacc[n], mka[0], mka[1], 0u, 0u, qs.x, 0u);
-      mma_f16(sacc[n], mka[0], mka[1], 0u, 0u, qs.y, 0u);
+      if constexpr (QSUM == 0) {
+        mma_f16(sacc[n], mka[0], mka[1], 0u, 0u, qs.x, 0u);
+        mma_f16(sacc[n], mka[0], mka[1], 0u, 0u, qs.y, 0u);
+      } else {
+        float xh[4], xl[4];
+        mma_f16_z(xh, mka[0], mka[1], 0u, 0u, qs.x, 0u);
+        mma_f16_z(xl, mka[0], mka[1], 0u, 0u, qs.y, 0u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sacc[n][e] = fmaf(static_cast<float>(1 << QSUM), fmaf(0x1p-11f, xl[e], xh[e]), sacc[n][e]);
+      }
     }
   }
 }
@@ -279,19 +289,19 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g
 // lane % 4; the thread's rows are 2t, 2t + 1).
 //   QP           f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
 //   qfrag(b, f)  fills f[k-step] with the query's B fragments of block b (hi0, hi1, lo0, lo1)
-//   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment
+//   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment (tile_scores)
 //   crow         turns a dot product with the normalised row into a base-2 softmax score
 //   grow         how far, in powers of two, a score may pass the running maximum (p <= 2^grow)
 //   mask(e, x)   x, or -inf where the key is unseen: token g + 8 (e / 2), row 2t + e % 2
 // The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
-template <typename L, int KF, int VF, int QP, typename QFrag, typename Mask>
+template <typename L, int KF, int VF, int QP, int QSUM, typename QFrag, typename Mask>
 __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
                                             uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], float grow,
                                             Mask mask, float (&m_run)[2], float (&l_run)[2],
                                             float (&oacc)[2 * kTileBlocks][4], float (&racc)[4]) {
   using F = TileFormat<KF, VF>;
   float sacc[1][4];
-  tile_scores<L, KF, VF, QP, 1>(
+  tile_scores<L, KF, VF, QP, QSUM, 1>(
       kb, G, g, t, [&](int, int bl, uint4 (&f)[2]) { qfrag(bl, f); }, [&](int) { return make_uint2(qsb_hi, qsb_lo); },
       sacc);
   // ---------------- online softmax (base 2) ----------------

@@ -155,6 +155,31 @@ def test_outputs_of_16_bits_are_rounded_once(kv_gpu, name, group):
             assert (out[s] != nearest).sum() <= allowed + 5 * allowed ** 0.5 + 5, (k_fmt, v_fmt)
 
 
+@pytest.mark.parametrize("name,spread", [("float16", 2.0 ** 28), ("bfloat16", 2.0 ** 24), ("float32", 2.0 ** 12)])
+@pytest.mark.parametrize("k_fmt,v_fmt", [("q8_0", "q4_0"), ("q5_1", "q8_0"), ("q4_0", "q4_0")])
+def test_queries_with_one_loud_channel(kv_gpu, name, spread, k_fmt, v_fmt):
+    """A channel of the query `spread` times the others, where every key is zero: the others make the scores."""
+    rng = np.random.default_rng(10)
+    T = 300
+    for group in (3, 12):
+        k, v, q = history(rng, T, 1.0, 0.0, 0, 1.0, group)
+        k[:, 32:64] = 0
+        q = np.sign(q) * np.clip(np.abs(q), 0.25, 3)
+        q[..., 40] = 2.0
+        # fp16: from the bottom of the type to its top; the keys make up for the small queries
+        low = 2.0 ** -14 if name == "float16" else 1.0
+        q = (q * low).astype(np.float32)
+        q[..., 40] *= spread
+        for keys in (k / low, np.clip(k, -3, 3) / low):  # (with Q5_1 some of the first are past fp16's range)
+            c = History(kv_gpu, group, k_fmt, v_fmt, keys.astype(np.float32), v)
+            assert (c.held[0][:, 40] == 0).all()
+            qx = rounded(q, name)[0]
+            ref = c.exact(qx[0])
+            out, lse = c.decode(kv_gpu, name, 2, 0, qx)
+            for s in range(2):
+                c.check(out[s], lse[s], ref, name)
+
+
 # ------------------------------------------------------------- the shares of the work
 @pytest.mark.parametrize("name", ["float32", "bfloat16"])
 def test_ring_fills_over_a_pages_end(kv_gpu, name):
