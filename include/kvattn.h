@@ -188,9 +188,11 @@ KVATTN_API int kvattn_quantize_append(const kvattn_kv_desc* desc, const float* k
  *   lse          device fp32 [n_q][H_q]: natural-log log-sum-exp of the scaled scores
  *                (-inf and out = 0 for a row that sees no key)
  * Key and value codes enter the tensor-core MMAs exactly; block scales are applied in fp32
- * (keys) or folded into P as an exact f16 product plus a remainder (values), and the query
+ * (keys) or folded into P as an f16 product plus its remainder (values), and the query
  * and P are split into f16 high and low parts, so the result matches exact attention over
- * the dequantized cache to about 2^-20 relative.
+ * the dequantized cache to about 2^-20 of sum p |v|.  The parts end 2^-37 below the row's largest
+ * weight, times the larger of 1 and the largest value scale (weights), and 2^-36 below the largest
+ * weight times the largest scale (their products with the scales).
  *   ws, ws_bytes device workspace of at least kvattn_decode_workspace_size() bytes (256-byte
  *                aligned; may be NULL when that size is 0).  The keys of each KV head are
  *                split across CTAs; per-split (o, lse) partials go to the workspace and a
@@ -495,7 +497,7 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
  *                out = 0)
  *   ws           device workspace of kvattn_decode_batch_workspace_size() bytes, 256-byte
  *                aligned; needs no initialisation.  Calls that share one must not overlap.
- * Accuracy: as kvattn_decode (about 2^-20 relative) before the output's own rounding.  Queries: fp16 rows
+ * Accuracy: as kvattn_decode (about 2^-20 of sum p |v|) before the output's own rounding.  Queries: fp16 rows
  * and bf16 elements within 2^-32 of their row's largest are exact, fp32 elements within 2^-17 of it keep 22
  * bits; smaller ones are held to 2^-39 of the largest.
  * Supports group * max_rows <= 24 and n_seqs * H_kv * max_blocks <= 2^27 (table entries).

@@ -126,6 +126,7 @@ struct alignas(16) WideState {
   float crow[8 * NR];
   int qpos[8 * NR];
   float top[4][8 * NR], sum[4][8 * NR];  // of each warp
+  uint32_t scale[4];                     // the largest value scale of each warp's tile
   uint2 qsums[NR][32];                   // zero-point keys: block sums as B fragments
 };
 
@@ -563,6 +564,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
     // ---- the tiles
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     float oacc[2 * kTileBlocks][4], racc[4] = {0.f, 0.f, 0.f, 0.f};
+    ValueScale vs;
 #pragma unroll
     for (int i = 0; i < 2 * kTileBlocks; ++i)
 #pragma unroll
@@ -586,18 +588,19 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
         }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
         attend_tile<L, KF, VF, QP, QSUM>(
-            kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow, 2.f,
+            kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
               return need_mask && (at > qpos[e & 1] || at <= qpos[e & 1] - span) ? -INFINITY : x;
             },
-            m_run, l_run, oacc, racc);
+            vs, m_run, l_run, oacc, racc);
       }
       __syncwarp();
       issue(k + C::kStages);
     }
 
     // ---- rows 2t, 2t + 1, dims 16 i + g, + 8
+    float unit = vs.unit();  // of oacc
     if constexpr (F::kVMin) {
       // zero-point values: the minimum terms of block b for rows 2t, 2t + 1 sit in lane 4b + t
 #pragma unroll
@@ -607,10 +610,11 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
           const float v = __shfl_sync(0xffffffffu, racc[c], 4 * b + t);
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb) {
-            oacc[2 * b + hb][c] += v;
-            oacc[2 * b + hb][c + 2] += v;
+            oacc[2 * b + hb][c] = fmaf(oacc[2 * b + hb][c], unit, v);
+            oacc[2 * b + hb][c + 2] = fmaf(oacc[2 * b + hb][c + 2], unit, v);
           }
         }
+      unit = 1.f;
     }
     BatchUnit w;  // the unit again
     w.unit = lds_int(&mine->unit);
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       // a row that saw no key: l = 0 (a NaN stays one)
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : unit / l;
       const float lse2 = l == 0.f ? -INFINITY : m_run[c] + log2f(l);
       const int row = 2 * t + c;
       if (row >= n_rows) continue;
@@ -799,6 +803,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
     }
     const int last = un.pos0 + un.rows - 1, pos0 = un.pos0;
     const int span = p.window > 0 ? p.window : INT_MAX;
+    ValueScale vs;
 
     for (; k < end; k += 4, ++step) {
       const int st = step % C::kStages;
@@ -808,11 +813,13 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       const uint32_t kb = ring_s + st * C::kStepBytes + w * C::kTileBytes;
       const bool live = k + w < end && key >= 0;
       float sv[NR][4];
+      uint2 dv = make_uint2(0u, 0u);  // value scales of block g, tokens 2t, + 1, + 8, + 9
       if (live) {
         if (key + 15 > last) {
           uint8_t* vs = ring + st * C::kStepBytes + w * C::kTileBytes + L::kV + L::kVScale;
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
+        dv = lds_pair(kb + L::kV + L::kVScale + (t * 8 + g) * 8);
         tile_scores<L, KF, VF, QP, QSUM, NR>(
             kb, 0, g, t,
             [&](int n, int bl, uint4 (&f)[2]) { load_qfrag<QP>(q_s + n * C::kQTileBytes, bl, lane, f); },
@@ -837,12 +844,12 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sv[n][e] = -INFINITY;
       }
-      // ---- the running maxima (within 2^2 of the rows' own, as in the one-warp kernel)
-      uint32_t need = 0;
+      // ---- the rows' references and the scales' powers of two, as in the one-warp kernel
+      uint32_t need = exceeds(dv.x, dv.y, vs.bound);
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) need |= fmaxf(sv[n][c], sv[n][c + 2]) > m_run[n][c] + 2.f;
+        for (int c = 0; c < 2; ++c) need |= fmaxf(sv[n][c], sv[n][c + 2]) > m_run[n][c] + vs.top;
       asm volatile(
           "{\n\t.reg .pred p, q;\n\t"
           "setp.ne.u32 q, %1, 0;\n\t"
@@ -854,6 +861,8 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       // every warp is done with the step before this one: its stage takes the step S - 1 ahead
       issue((step + C::kStages - 1) % C::kStages);
       if (need) {
+        const uint32_t own = largest_scale(dv);
+        if (lane == 0) state->scale[w] = own;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -865,6 +874,11 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
             if (g == 0) state->top[w][8 * n + 2 * t + c] = mx;
           }
         group_sync();
+        const uint4 scale = lds128(smem_u32(state->scale));
+        const float top = vs.top;
+        int dk;
+        float ratio;
+        vs.raise(max(max(scale.x, scale.y), max(scale.z, scale.w)), &dk, &ratio);
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -872,17 +886,16 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
             const int row = 8 * n + 2 * t + c;
             const float mx = fmaxf(fmaxf(state->top[0][row], state->top[1][row]),
                                    fmaxf(state->top[2][row], state->top[3][row]));
-            if (mx > m_run[n][c] + 2.f) {
-              const float alpha = fast_exp2(m_run[n][c] - mx);  // 0 when m_run = -inf
-              l_run[n][c] *= alpha;
+            const float m = mx > m_run[n][c] + top ? mx + (kGrow - vs.top) : m_run[n][c] + static_cast<float>(dk);
+            const float alpha = m == m_run[n][c] ? 1.f : fast_exp2(m_run[n][c] - m);  // 0 when m_run = -inf
+            l_run[n][c] *= alpha;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                oacc[i][n][c] *= alpha;
-                oacc[i][n][c + 2] *= alpha;
-              }
-              if constexpr (F::kVMin) racc[n][c] *= alpha;
-              m_run[n][c] = mx;
+            for (int i = 0; i < 4; ++i) {
+              oacc[i][n][c] *= alpha * ratio;
+              oacc[i][n][c + 2] *= alpha * ratio;
             }
+            if constexpr (F::kVMin) racc[n][c] *= alpha;
+            m_run[n][c] = m;
           }
       }
       // ---- P, as B fragments
@@ -896,14 +909,15 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           pr[c + 2] = fast_exp2(sv[n][c + 2] - mu);
           l_run[n][c] += pr[c] + pr[c + 2];
         }
-        const uint32_t to = p_s + w * C::kPTileBytes + (n * 32 + lane) * C::kPFragBytes;
         uint32_t h01, l01, h23, l23;
         split_pair(pr[0], pr[1], h01, l01);
         split_pair(pr[2], pr[3], h23, l23);
-        sts128(to, movmatrix_t(h01), movmatrix_t(h23), movmatrix_t(l01), movmatrix_t(l23));
+        sts128(p_s + w * C::kPTileBytes + (n * 32 + lane) * C::kPFragBytes, movmatrix_t(h01), movmatrix_t(h23),
+               movmatrix_t(l01), movmatrix_t(l23));
       }
       group_sync();
       // ---- O^T += V^T P^T for this warp's channels, over the step's tiles
+      const uint32_t mul = vs.mul();
       auto add_values = [&](int u) {
         const uint32_t vb = ring_s + st * C::kStepBytes + u * C::kTileBytes + L::kV;
         uint32_t ph[NR][2], pl[NR][2];
@@ -915,6 +929,8 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
         int e = 0;  // constant in the unrolled code
         tile_value_pair<L, KF, VF>(
             vb, 0, w, g, t, [&](int, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
+              d0 = hmul2(d0, mul);
+              d1 = hmul2(d1, mul);
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
                 uint32_t bh0, bl0, bh1, bl1;
@@ -928,14 +944,11 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
               ++e;
             });
         if constexpr (F::kVMin) {
-          uint32_t m01, m89;
-          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                       : "=r"(m01), "=r"(m89)
-                       : "r"(vb + L::kVMinimum + ((t * 8 + g) * 4) * 2));
+          const uint2 mw = lds_pair(vb + L::kVMinimum + (t * 8 + g) * 8);
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            mma_f16(racc[n], m01, 0u, m89, 0u, ph[n][0], ph[n][1]);
-            mma_f16(racc[n], m01, 0u, m89, 0u, pl[n][0], pl[n][1]);
+            mma_f16(racc[n], mw.x, 0u, mw.y, 0u, ph[n][0], ph[n][1]);
+            mma_f16(racc[n], mw.x, 0u, mw.y, 0u, pl[n][0], pl[n][1]);
           }
         }
       };
@@ -966,6 +979,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         if (g == 0) state->sum[w][8 * n + 2 * t + c] = l;
       }
+    float unit = vs.unit();  // of oacc
     if constexpr (F::kVMin) {
       // the minimum terms of block b for rows 2t, 2t + 1 sit in lane 4b + t
 #pragma unroll
@@ -977,10 +991,11 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
             const float v = __shfl_sync(0xffffffffu, racc[n][c], 4 * (2 * w + e) + t);
 #pragma unroll
             for (int i = 2 * e; i < 2 * e + 2; ++i) {
-              oacc[i][n][c] += v;
-              oacc[i][n][c + 2] += v;
+              oacc[i][n][c] = fmaf(oacc[i][n][c], unit, v);
+              oacc[i][n][c + 2] = fmaf(oacc[i][n][c + 2], unit, v);
             }
           }
+      unit = 1.f;
     }
     group_sync();
     BatchUnit wk;  // the unit again
@@ -999,7 +1014,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
         if (row >= n_rows) continue;
         const float l = (state->sum[0][row] + state->sum[1][row]) + (state->sum[2][row] + state->sum[3][row]);
         // a row that saw no key: l = 0 (a NaN stays one)
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : unit / l;
         const float lse2 = l == 0.f ? -INFINITY : m_run[n][c] + log2f(l);
         if (whole) {
           const int qi = row / p.group, hq = wk.h * p.group + row - qi * p.group;

@@ -20,12 +20,12 @@
 //         block's fp16 scale in fp32 (plus minimum x query block sum for zero-point keys).
 //   PV:   f16 MMA (m16n8k16), A = V^T codes decoded in registers (exact), B = P^T (fp32
 //         probabilities split into f16 high and low parts, transposed in registers with
-//         movmatrix) times the per-token V block scale, again as an exact-product high part
-//         and a low part.  Zero-point values add sum_t p_t m_t per block through an all-ones
-//         A operand.
-// The online softmax keeps a per-row running maximum and rescales the accumulators only
-// when the maximum grows by more than 2^8 (p stays <= 256, safe in f16); the exact
-// cross-lane maximum is only computed when a warp vote says some score crossed that bound.
+//         movmatrix) times the per-token V block scale, again as a high part and a low part,
+//         both factors as high in f16 as they fit (decode_tile.cuh, ValueScale).  Zero-point
+//         values add sum_t p_t m_t per block through an MMA whose A operand is the minima.
+// The online softmax keeps a reference per row, a power of two below its running maximum, and
+// rescales the accumulators only when the maximum grows by more than 2^2 or a larger value
+// scale comes along; the exact cross-lane maximum is only computed when a warp vote says so.
 // Warps merge their partial states in shared memory; CTAs write (o, lse) partials that a
 // small follow-up grid (programmatic dependent launch) merges by log-sum-exp, the arithmetic
 // of kvattn_merge_lse.
@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(DecodeCfg<KF, VF, NT>::kThreads, 1) decode_ker
   // from oacc (every dimension of a block gets the same term) and added at the end; an MMA
   // accumulator with the 8 blocks as M (rows g: block g, rows g + 8 unused)
   float racc[4] = {0.f, 0.f, 0.f, 0.f};
+  ValueScale vs;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     m_run[c] = -INFINITY;
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(DecodeCfg<KF, VF, NT>::kThreads, 1) decode_ker
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int rr = nt0 * 8 + 2 * t + c;
-      qpos_row[c] = rr < n_rows ? p.q_pos[rr / p.group] : INT_MAX;
+      qpos_row[c] = p.q_pos[rr < n_rows ? rr / p.group : 0];  // (a row past the last sees what the first does)
     }
     const uint32_t q_s = smem_u32(smem + C::kQOffset);
     {
@@ -384,11 +385,11 @@ __global__ void __launch_bounds__(DecodeCfg<KF, VF, NT>::kThreads, 1) decode_ker
           }
           const int key0 = logical * kPageTokens + 16 * G + g;  // rows e<2: token g, e>=2: g+8
           attend_tile<PageLayout<KF, VF>, KF, VF, 2, 0>(
-              kb, vb, G, g, t, qfrag, qsb_hi, qsb_lo, crow, 8.f,
+              kb, vb, G, g, t, qfrag, qsb_hi, qsb_lo, crow,
               [&](int e, float x) {
                 return need_mask && key0 + 8 * (e >> 1) > qpos_row[e & 1] ? -INFINITY : x;
               },
-              m_run, l_run, oacc, racc);
+              vs, m_run, l_run, oacc, racc);
         }
       }
       __syncwarp();
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(DecodeCfg<KF, VF, NT>::kThreads, 1) decode_ker
 
   // ---------------- merge the CTA's softmax streams in shared memory ----------------
   // one stream per warp, over the 8 rows of its n-tile (local row lr = row % 8):
-  // ms[warp][lr], ls[warp][lr], os[warp][lr][kOStride]  (all fp32)
+  // ms[warp][lr], ls[warp][lr], os[warp][lr][kOStride]  (all fp32; ms is the row's reference)
   float* ms = reinterpret_cast<float*>(smem);
   float* ls = ms + C::kConsumerWarps * 8;
   float* os = ls + C::kConsumerWarps * 8;
@@ -448,6 +449,7 @@ __global__ void __launch_bounds__(DecodeCfg<KF, VF, NT>::kThreads, 1) decode_ker
         ls[warp * 8 + 2 * t + c] = l_run[c];
       }
     }
+    const float unit = vs.unit();
 #pragma unroll
     for (int mt = 0; mt < 2 * C::kNB; ++mt) {
       const int b = mt >> 1, hb = mt & 1;
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(DecodeCfg<KF, VF, NT>::kThreads, 1) decode_ker
       for (int e = 0; e < 4; ++e) {
         const int lr = 2 * t + (e & 1);
         const int dim = 32 * b + 16 * hb + g + 8 * (e >> 1);
-        float v = oacc[mt][e];
+        float v = oacc[mt][e] * unit;
         if constexpr (F::kVMin) v += rv[mt >> 1][e & 1];
         os[(warp * 8 + lr) * C::kOStride + dim] = v;
       }

@@ -52,9 +52,9 @@ constexpr uint32_t kHalf2_m80 = 0xD500D500u;   // -(64 + 16)
 constexpr uint32_t kHalf2_Sign = 0x80008000u;
 
 // B operand (probabilities times a per-token fp16 factor f) as an unevaluated f16 sum hi + lo:
-// hi = f16(ph * f); ph * f - hi is exact in f16 (an 11 x 11-bit product rounded to 11 bits
-// leaves at most 11 bits), and lo adds pl * f with one rounding.  hi + lo equals (ph + pl) * f
-// to about 2^-22 relative.
+// hi = f16(ph * f); ph * f - hi is an 11 x 11-bit product without its first 11 bits, and lo adds
+// pl * f with one rounding.  hi + lo equals (ph + pl) * f to about 2^-22 relative, and to 2^-24 (f16's
+// smallest step, once for the remainder and once for lo) where that is more.
 __device__ __forceinline__ void split_scaled(uint32_t ph, uint32_t pl, uint32_t f, uint32_t& hi, uint32_t& lo) {
   hi = hmul2(ph, f);
   lo = hfma2(pl, f, hfma2(ph, f, hi ^ kHalf2_Sign));
@@ -64,6 +64,12 @@ __device__ __forceinline__ void split_scaled(uint32_t ph, uint32_t pl, uint32_t 
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = pack_half2(x0, x1);
   lo = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
+}
+
+__device__ __forceinline__ uint2 lds_pair(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
 }
 
 // Where the parts of a page sit in a shared-memory copy: a whole page (tile G of it is read) ...
@@ -95,7 +101,6 @@ struct SingleTileLayout {
 //   qfrag(n, b, f) fills f[k-step] with the B fragments of n-tile n, block b (hi0, hi1, lo0, lo1)
 //   qsums(n)       zero-point keys: the query's block sums as a B fragment (hi, lo); with QSUM > 0 divided by
 //                  2^QSUM, and lo times 2^11
-// (Interleaving the MMAs of two blocks measured no faster in any kernel, for 12 more registers.)
 // The tile is tile G of the copy at kb, arranged as L.
 template <typename L, int KF, int VF, int QP, int QSUM, int NR, typename QFrag, typename QSums>
 __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QFrag qfrag, QSums qsums,
@@ -285,19 +290,82 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g
   }
 }
 
+// ---- the powers of two of P x scale.  The second MMA takes P times a value's scale as f16 parts, and f16
+// ends at 2^-24: both factors are put as high in it as they fit, by powers of two that the sums carry.
+//   P       is relative to a reference of the row, kPTop - k below the row's running maximum (which may
+//           lag 2^kGrow behind): the largest P is 2^kPTop to 2^(kPTop + kGrow) = 2^15 for k = 0
+//   scales  are multiplied by `mul`, so that the largest so far comes to (1/2, 1]; where it is above 1
+//           they stay as they are, and k is its exponent instead (a small scale then keeps its bits)
+// The products' two parts so end about 2^37 below the row's largest P times the largest scale.
+// (Both are one state of all rows and channels that a warp, or a group of warps, adds up.  It moves when a
+// larger scale comes along: seldom after the first tiles.)
+constexpr float kPTop = 13.f, kGrow = 2.f;
+
+struct ValueScale {
+  uint32_t bound = 0u;          // twice the f16 power of two that no scale so far exceeds (0: none seen)
+  float top = kPTop + kGrow;    // how far a score may pass its row's reference: kPTop + kGrow - k
+  __device__ __forceinline__ uint32_t mul() const { return 0x78007800u - min(bound, 0x3C003C00u); }
+  // the exponent of the bound, + 15 (2^16 is kept as the largest f16 instead, so that infinities exceed it)
+  __device__ __forceinline__ int exponent() const { return static_cast<int>((bound & 0xFFFFu) + 0x3FFu) >> 10; }
+  // what undoes mul() in a sum
+  __device__ __forceinline__ float unit() const { return exp2_int(min(exponent(), 15) - 15); }
+  __device__ __forceinline__ static float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+  // Takes in scales up to `most` (f16 bits): the new exponent of two of the rows' references goes to *k, the
+  // factor of the sums of P x scale beside it to *ratio.
+  __device__ __forceinline__ void raise(uint32_t most, int* dk, float* ratio) {
+    const int was = exponent();
+    int now = was;
+    if (most > (bound & 0xFFFFu)) now = most < 0x400u ? 1 : static_cast<int>(most + 0x3FFu) >> 10;
+    *dk = max(now - 15, 0) - max(was - 15, 0);
+    *ratio = exp2_int(min(was, 15) - min(now, 15));
+    bound = min(static_cast<uint32_t>(now) << 10, 0x7BFFu) * 0x00010001u;
+    top -= static_cast<float>(*dk);
+  }
+};
+
+// Whether one of the two f16 pairs has an element whose magnitude exceeds bound's (NaN exceeds all).
+__device__ __forceinline__ bool exceeds(uint32_t a, uint32_t b, uint32_t bound) {
+  uint32_t over;
+  asm("{\n\t.reg .b32 x, y;\n\t.reg .pred p, q;\n\t"
+      "abs.f16x2 x, %1;\n\t"
+      "abs.f16x2 y, %2;\n\t"
+      "max.NaN.f16x2 x, x, y;\n\t"
+      "setp.gtu.f16x2 p|q, x, %3;\n\t"
+      "or.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(over)
+      : "r"(a), "r"(b), "r"(bound));
+  return over != 0;
+}
+
+// The largest of a tile's scales that are finite, as f16 bits; lane (g, t) holds four of them.
+__device__ __forceinline__ uint32_t largest_scale(uint2 d) {
+  const uint32_t w[2] = {d.x, d.y};
+  uint32_t most = 0;
+#pragma unroll
+  for (int H = 0; H < 2; ++H)
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {
+      const uint32_t x = (w[H] >> (16 * odd)) & 0x7FFFu;
+      if (x < 0x7C00u) most = max(most, x);
+    }
+  return __reduce_max_sync(0xffffffffu, most);
+}
+
 // Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
 // lane % 4; the thread's rows are 2t, 2t + 1).
 //   QP           f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
 //   qfrag(b, f)  fills f[k-step] with the query's B fragments of block b (hi0, hi1, lo0, lo1)
 //   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment (tile_scores)
 //   crow         turns a dot product with the normalised row into a base-2 softmax score
-//   grow         how far, in powers of two, a score may pass the running maximum (p <= 2^grow)
 //   mask(e, x)   x, or -inf where the key is unseen: token g + 8 (e / 2), row 2t + e % 2
+//   m_run        the rows' references (above), vs the scales' state; l_run, oacc and racc are sums relative to
+//                them: of P, of P x scale x code (x vs.mul()) and of P x minimum
 // The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
 template <typename L, int KF, int VF, int QP, int QSUM, typename QFrag, typename Mask>
 __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
-                                            uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], float grow,
-                                            Mask mask, float (&m_run)[2], float (&l_run)[2],
+                                            uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], Mask mask,
+                                            ValueScale& vs, float (&m_run)[2], float (&l_run)[2],
                                             float (&oacc)[2 * kTileBlocks][4], float (&racc)[4]) {
   using F = TileFormat<KF, VF>;
   float sacc[1][4];
@@ -305,12 +373,13 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
       kb, G, g, t, [&](int, int bl, uint4 (&f)[2]) { qfrag(bl, f); }, [&](int) { return make_uint2(qsb_hi, qsb_lo); },
       sacc);
   // ---------------- online softmax (base 2) ----------------
-  // The running maximum m_run of a row is shared by the 8 lanes that hold the row.
-  // It only has to bound the scores to within 2^grow (p <= 2^grow in f16), so the exact
-  // cross-lane maximum is computed only when some lane sees a score above
-  // m_run + grow: one warp vote per tile instead of three shuffles per row.
+  // The reference m_run of a row is shared by the 8 lanes that hold the row.  It only has to be
+  // within 2^kGrow of what the running maximum asks for, so the exact cross-lane maximum is computed
+  // only when some lane sees a score above it: one warp vote per tile (which the scales of the
+  // tile's values share) instead of three shuffles per row.
+  const uint2 dv = lds_pair(vb + L::kVScale + ((G * 4 + t) * 8 + g) * 8);  // block g, tokens 2t, + 1, + 8, + 9
   float sv[4], lm[2];
-  bool need = false;
+  bool need = exceeds(dv.x, dv.y, vs.bound);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     sv[e] = mask(e, sacc[0][e] * crow[e & 1]);
@@ -318,39 +387,42 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     lm[c] = fmaxf(sv[c], sv[c + 2]);
-    need |= lm[c] > m_run[c] + grow;
+    need |= lm[c] > m_run[c] + vs.top;
   }
   if (__any_sync(0xffffffffu, need)) {
+    const float top = vs.top;
+    int dk;
+    float ratio;
+    vs.raise(largest_scale(dv), &dk, &ratio);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float mx = lm[c];
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      if (mx > m_run[c] + grow) {
-        const float alpha = fast_exp2(m_run[c] - mx);  // 0 when m_run = -inf
-        l_run[c] *= alpha;
+      const float m = mx > m_run[c] + top ? mx + (kGrow - vs.top) : m_run[c] + static_cast<float>(dk);
+      const float alpha = m == m_run[c] ? 1.f : fast_exp2(m_run[c] - m);  // 0 when m_run = -inf
+      l_run[c] *= alpha;
 #pragma unroll
-        for (int mt = 0; mt < 2 * kTileBlocks; ++mt) {
-          oacc[mt][c] *= alpha;
-          oacc[mt][c + 2] *= alpha;
-        }
-        if constexpr (F::kVMin) racc[c] *= alpha;
-        m_run[c] = mx;
+      for (int mt = 0; mt < 2 * kTileBlocks; ++mt) {
+        oacc[mt][c] *= alpha * ratio;
+        oacc[mt][c + 2] *= alpha * ratio;
       }
+      if constexpr (F::kVMin) racc[c] *= alpha;
+      m_run[c] = m;
     }
   }
   // P as f16 parts, transposed in registers into B fragments
   uint32_t pbh[2], pbl[2];
-  {
-    float pr[4];
+  float pr[4];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float mu = m_run[c] == -INFINITY ? 0.f : m_run[c];
-      pr[c] = fast_exp2(sv[c] - mu);
-      pr[c + 2] = fast_exp2(sv[c + 2] - mu);
-      l_run[c] += pr[c] + pr[c + 2];
-    }
+  for (int c = 0; c < 2; ++c) {
+    const float mu = m_run[c] == -INFINITY ? 0.f : m_run[c];
+    pr[c] = fast_exp2(sv[c] - mu);
+    pr[c + 2] = fast_exp2(sv[c + 2] - mu);
+    l_run[c] += pr[c] + pr[c + 2];
+  }
+  {
     uint32_t h01, l01, h23, l23;
     split_pair(pr[0], pr[1], h01, l01);
     split_pair(pr[2], pr[3], h23, l23);
@@ -360,15 +432,16 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
     pbl[1] = movmatrix_t(l23);
   }
   // ---------------- O^T += V^T P^T ----------------
-  // V codes enter the MMA exactly; the per-token block scale multiplies P (in two f16
-  // parts), two MMAs per 16-dimension half.
+  // V codes enter the MMA exactly; the per-token block scale multiplies P (in two f16 parts),
+  // two MMAs per 16-dimension half.
+  const uint32_t mul = vs.mul();
 #pragma unroll
   for (int C = 0; C < kTileBlocks / 2; ++C)
     tile_value_pair<L, KF, VF>(vb, G, C, g, t,
                                [&](int bl, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
       uint32_t bh0, bl0, bh1, bl1;
-      split_scaled(pbh[0], pbl[0], d0, bh0, bl0);
-      split_scaled(pbh[1], pbl[1], d1, bh1, bl1);
+      split_scaled(pbh[0], pbl[0], hmul2(d0, mul), bh0, bl0);
+      split_scaled(pbh[1], pbl[1], hmul2(d1, mul), bh1, bl1);
       mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
       mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
       mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
@@ -378,12 +451,9 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
     // sum over the tile's tokens of p * m for all 8 blocks at once: A = the minima
     // (block g x tokens 2t, 2t + 1 | 2t + 8, 2t + 9, exact in f16; blocks 8..15 zero),
     // B = P^T as its high and low parts
-    uint32_t m01, m89;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                 : "=r"(m01), "=r"(m89)
-                 : "r"(vb + L::kVMinimum + (((G * 4 + t) * 8 + g) * 4) * 2));
-    mma_f16(racc, m01, 0u, m89, 0u, pbh[0], pbh[1]);
-    mma_f16(racc, m01, 0u, m89, 0u, pbl[0], pbl[1]);
+    const uint2 m = lds_pair(vb + L::kVMinimum + ((G * 4 + t) * 8 + g) * 8);
+    mma_f16(racc, m.x, 0u, m.y, 0u, pbh[0], pbh[1]);
+    mma_f16(racc, m.x, 0u, m.y, 0u, pbl[0], pbl[1]);
   }
 }
 

@@ -133,6 +133,90 @@ def history(rng, T, spread, mean, logit, q_scale, group):
     return k, v, q.astype(np.float32)
 
 
+@pytest.mark.parametrize("v_fmt,spread,mean", [("q8_0", 0.1, 0.05), ("q4_0", 0.03, 0.01), ("q8_0", 1e-3, 4e-4),
+                                               ("q4_1", 1.0, 0.5), ("q4_1", 1e-2, 5e-3)])
+@pytest.mark.parametrize("logit", [0, 8, 12, 16])
+@pytest.mark.parametrize("group", [6, 20])
+def test_values_behind_a_dominant_key(kv_gpu, v_fmt, spread, mean, logit, group):
+    """An attention sink in position 0: the other keys' weights are far below 1 and their small values
+    make the answer.  The history in one warp group's stretch, and cut into many; the answers agree with each
+    other as with the definition."""
+    k_fmt = "q5_0" if v_fmt == "q4_1" else "q8_0"
+    k, v, q = history(np.random.default_rng(int(logit * 10 + group)), 4096, spread, mean, logit,
+                      2.0 if logit == 0 else 1.0, group)
+    c = History(kv_gpu, group, k_fmt, v_fmt, k, v)
+    for name in TYPES:
+        qx = rounded(q, name)[0]
+        ref = c.exact(qx[0])
+        for n_seqs, budget in ((1, 0), (26, 1)):
+            out, lse = c.decode(kv_gpu, name, n_seqs, budget, qx)
+            for s in range(n_seqs):
+                tol = c.check(out[s], lse[s], ref, name)
+            if name == "float32":  # zeros, or answers 1 % off, would not pass
+                assert (np.median(np.abs(ref[0]) / tol) > 100) or logit > 12
+
+
+@pytest.mark.parametrize("k_fmt,v_fmt", PAIRS)
+@pytest.mark.parametrize("amplitude", [1e-3, 1.0, 100.0, 6e4, 4e5])
+def test_amplitudes_of_values(kv_gpu, k_fmt, v_fmt, amplitude):
+    """Values from a thousandth to the top of what the formats hold."""
+    rng = np.random.default_rng(7)
+    for T, group in ((700, 4), (333, 12)):
+        k, v, q = history(rng, T, 1.0, 0.3, 0, 1.5, group)
+        # the largest scale stays below fp16's largest number: 8 (Q4_0), 127 (Q8_0) and 15 (Q4_1) codes a side
+        v *= min(amplitude, {"q4_0": 8, "q8_0": 127, "q4_1": 1}[v_fmt] * 65000) / np.abs(v).max()
+        c = History(kv_gpu, group, k_fmt, v_fmt, k, v)
+        for name in ("float32", "bfloat16"):
+            qx = rounded(q, name)[0]
+            ref = c.exact(qx[0])
+            out, lse = c.decode(kv_gpu, name, 3, 1, qx)
+            for s in range(3):
+                c.check(out[s], lse[s], ref, name)
+
+
+@pytest.mark.parametrize("group", [4, 16])
+def test_scales_that_grow_and_shrink(kv_gpu, group):
+    """Loud and quiet stretches of values in turn, in one group's stretch: the sums follow the loudest."""
+    rng = np.random.default_rng(8)
+    T = 2048
+    k, v, q = history(rng, T, 1.0, 0.2, 0, 1.0, group)
+    v *= np.repeat(10.0 ** np.array([-4, 0, 2, -2, 4, -5, 1, 3]), T // 8)[:, None].astype(np.float32)
+    for v_fmt in ("q8_0", "q4_0"):
+        c = History(kv_gpu, group, "q8_0", v_fmt, k, v)
+        for name in ("float32", "bfloat16"):
+            qx = rounded(q, name)[0]
+            ref = c.exact(qx[0])
+            out, lse = c.decode(kv_gpu, name, 14, 1, qx)
+            for s in range(14):
+                c.check(out[s], lse[s], ref, name)
+
+
+@pytest.mark.parametrize("n_q", [1, 4])
+@pytest.mark.parametrize("logit", [0, 8, 12])
+def test_single_sequence_decode_behind_a_dominant_key(kv_gpu, n_q, logit):
+    """The single-sequence call has the same arithmetic, on one SM's stretch and on all."""
+    import torch
+
+    kv = kv_gpu
+    rng = np.random.default_rng(9)
+    T, group = 4096, 6
+    k, v, q = history(rng, T, 0.1, 0.05, logit, 1.0, group)
+    q = np.repeat(q, n_q, 0)
+    for v_fmt in ("q8_0", "q4_0"):
+        c = History(kv, group, "q8_0", v_fmt, k, v)
+        ref = c.exact(q[0])
+        for budget in (0, 1):
+            c.desc.sm_budget = budget
+            out, lse = torch.zeros((n_q, group, 256), device="cuda"), torch.zeros((n_q, group), device="cuda")
+            pos = torch.full((n_q,), T - 1, dtype=torch.int32, device="cuda")
+            size = kv.kvattn_decode_workspace_size(c.desc, n_q, c.n)
+            ws = torch.zeros(max(size, 256), dtype=torch.uint8, device="cuda")
+            kv.kvattn_decode(c.desc, torch.from_numpy(q).cuda(), n_q, pos, c.table[0], None, None, c.n, out, lse, ws,
+                             size)
+            for i in range(n_q):
+                c.check(out[i].cpu().numpy(), lse[i].cpu().numpy(), ref, "float32")
+
+
 @pytest.mark.parametrize("name", ["float16", "bfloat16"])
 @pytest.mark.parametrize("group", [6, 20])
 def test_outputs_of_16_bits_are_rounded_once(kv_gpu, name, group):
