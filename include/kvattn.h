@@ -483,7 +483,8 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
 /* Attention of every row of the batch, for every query head, over the pages of its sequence.
  * A row at position P sees the keys at positions p <= P, and with window > 0 only those with
  * p > P - window.  Slots past the sequence's last position, and blocks that no row's window
- * reaches, are not used, whatever their bytes are.
+ * reaches, are not used, whatever their bytes are.  A value that is not finite (its scale or minimum
+ * past fp16's range) reaches the rows that see its key, in the channels of its block, and no other.
  *   q            [n_rows][H_q][256]
  *   page_logical device int32 [n_seqs][H_kv][max_blocks]: the logical block of each entry of
  *                page_table, which then is a list of pages in any order (a selection of

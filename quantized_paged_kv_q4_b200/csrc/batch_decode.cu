@@ -126,7 +126,7 @@ struct alignas(16) WideState {
   float crow[8 * NR];
   int qpos[8 * NR];
   float top[4][8 * NR], sum[4][8 * NR];  // of each warp
-  uint32_t scale[4];                     // the largest value scale of each warp's tile
+  uint32_t seen[4], all[4];              // of each warp's tile (tile_scale_range)
   uint2 qsums[NR][32];                   // zero-point keys: block sums as B fragments
 };
 
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
-        attend_tile<L, KF, VF, QP, QSUM>(
+        attend_tile<L, KF, VF, QP, QSUM, true>(
             kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
@@ -813,13 +813,14 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       const uint32_t kb = ring_s + st * C::kStepBytes + w * C::kTileBytes;
       const bool live = k + w < end && key >= 0;
       float sv[NR][4];
-      uint2 dv = make_uint2(0u, 0u);  // value scales of block g, tokens 2t, + 1, + 8, + 9
+      uint2 dv = make_uint2(0u, 0u), mv = make_uint2(0u, 0u);  // scales and minima of block g, tokens 2t, + 1, + 8, + 9
       if (live) {
         if (key + 15 > last) {
           uint8_t* vs = ring + st * C::kStepBytes + w * C::kTileBytes + L::kV + L::kVScale;
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
         dv = lds_pair(kb + L::kV + L::kVScale + (t * 8 + g) * 8);
+        if constexpr (F::kVMin) mv = lds_pair(kb + L::kV + L::kVMinimum + (t * 8 + g) * 8);
         tile_scores<L, KF, VF, QP, QSUM, NR>(
             kb, 0, g, t,
             [&](int n, int bl, uint4 (&f)[2]) { load_qfrag<QP>(q_s + n * C::kQTileBytes, bl, lane, f); },
@@ -846,6 +847,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       }
       // ---- the rows' references and the scales' powers of two, as in the one-warp kernel
       uint32_t need = exceeds(dv.x, dv.y, vs.bound);
+      if constexpr (F::kVMin) need |= exceeds(mv.x, mv.y, 0x7BFF7BFFu);
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -860,9 +862,18 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           : "memory");
       // every warp is done with the step before this one: its stage takes the step S - 1 ahead
       issue((step + C::kStages - 1) % C::kStages);
+      bool odd = false;
       if (need) {
-        const uint32_t own = largest_scale(dv);
-        if (lane == 0) state->scale[w] = own;
+        {
+          bool lo = false, hi = false;
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) lo |= sv[n][c] != -INFINITY, hi |= sv[n][c + 2] != -INFINITY;
+          uint32_t seen, all;
+          tile_scale_range<true>(dv, mv, lo, hi, t, &seen, &all);
+          if (lane == 0) state->seen[w] = seen, state->all[w] = all;
+        }
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -874,11 +885,12 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
             if (g == 0) state->top[w][8 * n + 2 * t + c] = mx;
           }
         group_sync();
-        const uint4 scale = lds128(smem_u32(state->scale));
+        const uint4 seen = lds128(smem_u32(state->seen)), all = lds128(smem_u32(state->all));
         const float top = vs.top;
         int dk;
         float ratio;
-        vs.raise(max(max(scale.x, scale.y), max(scale.z, scale.w)), &dk, &ratio);
+        vs.raise(max(max(seen.x, seen.y), max(seen.z, seen.w)), &dk, &ratio);
+        odd = max(max(all.x, all.y), max(all.z, all.w)) > (vs.bound & 0xFFFFu);
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -909,6 +921,10 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           pr[c + 2] = fast_exp2(sv[n][c + 2] - mu);
           l_run[n][c] += pr[c] + pr[c + 2];
         }
+        if (odd) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[e] = seen_p(pr[e], sv[n][e]);
+        }
         uint32_t h01, l01, h23, l23;
         split_pair(pr[0], pr[1], h01, l01);
         split_pair(pr[2], pr[3], h23, l23);
@@ -918,7 +934,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       group_sync();
       // ---- O^T += V^T P^T for this warp's channels, over the step's tiles
       const uint32_t mul = vs.mul();
-      auto add_values = [&](int u) {
+      auto add_values = [&](int u, auto odd_tile) {
         const uint32_t vb = ring_s + st * C::kStepBytes + u * C::kTileBytes + L::kV;
         uint32_t ph[NR][2], pl[NR][2];
 #pragma unroll
@@ -934,8 +950,8 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
                 uint32_t bh0, bl0, bh1, bl1;
-                split_scaled(ph[n][0], pl[n][0], d0, bh0, bl0);
-                split_scaled(ph[n][1], pl[n][1], d1, bh1, bl1);
+                scale_p<decltype(odd_tile)::value>(ph[n][0], pl[n][0], d0, bh0, bl0);
+                scale_p<decltype(odd_tile)::value>(ph[n][1], pl[n][1], d1, bh1, bl1);
                 mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
                 mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
                 mma_f16(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
@@ -945,10 +961,31 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
             });
         if constexpr (F::kVMin) {
           const uint2 mw = lds_pair(vb + L::kVMinimum + (t * 8 + g) * 8);
+          uint32_t m01 = mw.x, m89 = mw.y;
+          if constexpr (decltype(odd_tile)::value) {
+            // minima that are not finite, by hand (attend_tile): block g, rows 8n + 2t (+ 1); P of a
+            // row and token sits with lane (row, token / 2 % 4)
+            m01 &= finite_halves(m01);
+            m89 &= finite_halves(m89);
+#pragma unroll 1
+            for (int tok = 0; tok < 16; ++tok) {
+              const uint32_t word = lds32(vb + L::kVMinimum + (((tok & 7) / 2 * 8 + g) * 4 + 2 * (tok >> 3)) * 2);
+              const float x = tok & 1 ? half_hi(word) : half_lo(word);
+              if (fabsf(x) <= 65504.f) continue;
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const uint32_t pw = lds32(p_s + u * C::kPTileBytes +
+                                            (n * 32 + (2 * t + c) * 4 + (tok & 7) / 2) * C::kPFragBytes + 4 * (tok >> 3));
+                  if ((tok & 1 ? pw >> 16 : pw) & 0x7FFFu) racc[n][c] += x;
+                }
+            }
+          }
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            mma_f16(racc[n], mw.x, 0u, mw.y, 0u, ph[n][0], ph[n][1]);
-            mma_f16(racc[n], mw.x, 0u, mw.y, 0u, pl[n][0], pl[n][1]);
+            mma_f16(racc[n], m01, 0u, m89, 0u, ph[n][0], ph[n][1]);
+            mma_f16(racc[n], m01, 0u, m89, 0u, pl[n][0], pl[n][1]);
           }
         }
       };
@@ -956,14 +993,18 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(keys.x), "=r"(keys.y), "=r"(keys.z), "=r"(keys.w)
                    : "r"(smem_u32(key_of + 4 * st)));
-      if (k + 4 <= end && (keys.x | keys.y | keys.z | keys.w) >= 0) {
+      if (odd) {
+#pragma unroll 1
+        for (int u = 0; u < 4 && k + u < end; ++u)
+          if (lds_int(&key_of[4 * st + u]) >= 0) add_values(u, std::true_type{});
+      } else if (k + 4 <= end && (keys.x | keys.y | keys.z | keys.w) >= 0) {
         // all four are there: their loads and decoding overlap
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add_values(u);
+        for (int u = 0; u < 4; ++u) add_values(u, std::false_type{});
       } else {
 #pragma unroll 1
         for (int u = 0; u < 4 && k + u < end; ++u)
-          if (lds_int(&key_of[4 * st + u]) >= 0) add_values(u);
+          if (lds_int(&key_of[4 * st + u]) >= 0) add_values(u, std::false_type{});
       }
     }
     k = end;

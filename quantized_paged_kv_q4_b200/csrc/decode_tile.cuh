@@ -2,6 +2,8 @@
 // arithmetic, which the single-sequence and the ragged-batch decode share.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace kvattn {
@@ -64,6 +66,32 @@ __device__ __forceinline__ void split_scaled(uint32_t ph, uint32_t pl, uint32_t 
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = pack_half2(x0, x1);
   lo = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
+}
+
+// 0xFFFF in each half of x that is not zero / that is finite.
+__device__ __forceinline__ uint32_t nonzero_halves(uint32_t x) {
+  return ((x & 0x7FFFu) ? 0x0000FFFFu : 0u) | ((x & 0x7FFF0000u) ? 0xFFFF0000u : 0u);
+}
+__device__ __forceinline__ uint32_t finite_halves(uint32_t x) {
+  return ((x & 0x7C00u) != 0x7C00u ? 0x0000FFFFu : 0u) | ((x & 0x7C000000u) != 0x7C000000u ? 0xFFFF0000u : 0u);
+}
+
+// P of a key in a tile of odd scales: never 0 where the row sees the key (2^-24 is f16's smallest step), so
+// that a value which is not finite stays one, however small its weight.
+__device__ __forceinline__ float seen_p(float p, float score) {
+  return p < 0x1p-24f && score != -INFINITY ? 0x1p-24f : p;
+}
+
+// P (its f16 parts) times the per-token scales f of a block.  ODD: f may hold what is not finite, which
+// reaches the rows that see its key (P is not zero) and no other.
+template <bool ODD>
+__device__ __forceinline__ void scale_p(uint32_t ph, uint32_t pl, uint32_t f, uint32_t& hi, uint32_t& lo) {
+  split_scaled(ph, pl, f, hi, lo);
+  if constexpr (ODD) {
+    const uint32_t keep = nonzero_halves(ph);
+    hi &= keep;
+    lo &= keep;
+  }
 }
 
 __device__ __forceinline__ uint2 lds_pair(uint32_t addr) {
@@ -298,7 +326,7 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g
 //           they stay as they are, and k is its exponent instead (a small scale then keeps its bits)
 // The products' two parts so end about 2^37 below the row's largest P times the largest scale.
 // (Both are one state of all rows and channels that a warp, or a group of warps, adds up.  It moves when a
-// larger scale comes along: seldom after the first tiles.)
+// larger scale of a key that some row sees comes along: seldom after the first tiles.)
 constexpr float kPTop = 13.f, kGrow = 2.f;
 
 struct ValueScale {
@@ -338,23 +366,40 @@ __device__ __forceinline__ bool exceeds(uint32_t a, uint32_t b, uint32_t bound) 
   return over != 0;
 }
 
-// The largest of a tile's scales that are finite, as f16 bits; lane (g, t) holds four of them.
-__device__ __forceinline__ uint32_t largest_scale(uint2 d) {
-  const uint32_t w[2] = {d.x, d.y};
-  uint32_t most = 0;
+// The largest scale of a tile, as f16 bits, among the keys that some row sees and that are finite (*seen), and
+// among all (*all: 0xFFFF with a NaN or an infinity, of a minimum too).  Lane (g, t) holds the scales (and
+// minima) of block g, tokens 2t, 2t + 1 in the first word and 2t + 8, 2t + 9 in the second; lo and hi
+// say whether a row of the lane's sees token g, g + 8 (mma.sync's accumulator layout).
+template <bool ODD>
+__device__ __forceinline__ void tile_scale_range(uint2 d, uint2 m, bool lo, bool hi, int t, uint32_t* seen,
+                                                 uint32_t* all) {
+  uint32_t vis[2] = {0u, 0u};
+  if constexpr (ODD) {
+    vis[0] = __ballot_sync(0xffffffffu, lo);
+    vis[1] = __ballot_sync(0xffffffffu, hi);
+  }
+  const uint32_t w[2] = {d.x, d.y}, n[2] = {m.x, m.y};
+  uint32_t s = 0, a = 0;
 #pragma unroll
   for (int H = 0; H < 2; ++H)
 #pragma unroll
     for (int odd = 0; odd < 2; ++odd) {
-      const uint32_t x = (w[H] >> (16 * odd)) & 0x7FFFu;
-      if (x < 0x7C00u) most = max(most, x);
+      uint32_t x = (w[H] >> (16 * odd)) & 0x7FFFu;
+      const uint32_t y = (n[H] >> (16 * odd)) & 0x7FFFu;
+      const bool live = !ODD || ((vis[H] >> (8 * t + 4 * odd)) & 15u);
+      if (x < 0x7C00u && live) s = max(s, x);
+      if (x >= 0x7C00u || y >= 0x7C00u) x = 0xFFFFu;
+      a = max(a, x);
     }
-  return __reduce_max_sync(0xffffffffu, most);
+  *seen = __reduce_max_sync(0xffffffffu, s);
+  *all = ODD ? __reduce_max_sync(0xffffffffu, a) : 0u;
 }
 
 // Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
 // lane % 4; the thread's rows are 2t, 2t + 1).
 //   QP           f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
+//   ODD          whether values that are not finite stay with the rows that see their keys, and scales that no
+//                row sees are left out of vs.  Without it every finite scale of a tile counts.
 //   qfrag(b, f)  fills f[k-step] with the query's B fragments of block b (hi0, hi1, lo0, lo1)
 //   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment (tile_scores)
 //   crow         turns a dot product with the normalised row into a base-2 softmax score
@@ -362,7 +407,7 @@ __device__ __forceinline__ uint32_t largest_scale(uint2 d) {
 //   m_run        the rows' references (above), vs the scales' state; l_run, oacc and racc are sums relative to
 //                them: of P, of P x scale x code (x vs.mul()) and of P x minimum
 // The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
-template <typename L, int KF, int VF, int QP, int QSUM, typename QFrag, typename Mask>
+template <typename L, int KF, int VF, int QP, int QSUM, bool ODD, typename QFrag, typename Mask>
 __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
                                             uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], Mask mask,
                                             ValueScale& vs, float (&m_run)[2], float (&l_run)[2],
@@ -378,8 +423,10 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
   // only when some lane sees a score above it: one warp vote per tile (which the scales of the
   // tile's values share) instead of three shuffles per row.
   const uint2 dv = lds_pair(vb + L::kVScale + ((G * 4 + t) * 8 + g) * 8);  // block g, tokens 2t, + 1, + 8, + 9
+  const uint2 mv = F::kVMin ? lds_pair(vb + L::kVMinimum + ((G * 4 + t) * 8 + g) * 8) : make_uint2(0u, 0u);
   float sv[4], lm[2];
   bool need = exceeds(dv.x, dv.y, vs.bound);
+  if constexpr (F::kVMin && ODD) need |= exceeds(mv.x, mv.y, 0x7BFF7BFFu);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     sv[e] = mask(e, sacc[0][e] * crow[e & 1]);
@@ -389,11 +436,16 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
     lm[c] = fmaxf(sv[c], sv[c + 2]);
     need |= lm[c] > m_run[c] + vs.top;
   }
+  bool odd = false;  // a scale or minimum that is not finite, or a scale that no row sees above the bound
   if (__any_sync(0xffffffffu, need)) {
+    uint32_t seen, all;
+    tile_scale_range<ODD>(dv, mv, sv[0] != -INFINITY || sv[1] != -INFINITY, sv[2] != -INFINITY || sv[3] != -INFINITY, t,
+                          &seen, &all);
     const float top = vs.top;
     int dk;
     float ratio;
-    vs.raise(largest_scale(dv), &dk, &ratio);
+    vs.raise(seen, &dk, &ratio);
+    if constexpr (ODD) odd = all > (vs.bound & 0xFFFFu);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float mx = lm[c];
@@ -422,6 +474,10 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
     pr[c + 2] = fast_exp2(sv[c + 2] - mu);
     l_run[c] += pr[c] + pr[c + 2];
   }
+  if (odd) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pr[e] = seen_p(pr[e], sv[e]);
+  }
   {
     uint32_t h01, l01, h23, l23;
     split_pair(pr[0], pr[1], h01, l01);
@@ -435,25 +491,48 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
   // V codes enter the MMA exactly; the per-token block scale multiplies P (in two f16 parts),
   // two MMAs per 16-dimension half.
   const uint32_t mul = vs.mul();
+  auto add_values = [&](auto odd_tile) {
 #pragma unroll
-  for (int C = 0; C < kTileBlocks / 2; ++C)
-    tile_value_pair<L, KF, VF>(vb, G, C, g, t,
-                               [&](int bl, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
-      uint32_t bh0, bl0, bh1, bl1;
-      split_scaled(pbh[0], pbl[0], hmul2(d0, mul), bh0, bl0);
-      split_scaled(pbh[1], pbl[1], hmul2(d1, mul), bh1, bl1);
-      mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
-      mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
-      mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
-      mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
-    });
+    for (int C = 0; C < kTileBlocks / 2; ++C)
+      tile_value_pair<L, KF, VF>(vb, G, C, g, t,
+                                 [&](int bl, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
+        uint32_t bh0, bl0, bh1, bl1;
+        scale_p<decltype(odd_tile)::value>(pbh[0], pbl[0], hmul2(d0, mul), bh0, bl0);
+        scale_p<decltype(odd_tile)::value>(pbh[1], pbl[1], hmul2(d1, mul), bh1, bl1);
+        mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
+        mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
+        mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
+        mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
+      });
+  };
+  if (odd)
+    add_values(std::true_type{});
+  else
+    add_values(std::false_type{});
   if constexpr (F::kVMin) {
     // sum over the tile's tokens of p * m for all 8 blocks at once: A = the minima
     // (block g x tokens 2t, 2t + 1 | 2t + 8, 2t + 9, exact in f16; blocks 8..15 zero),
     // B = P^T as its high and low parts
-    const uint2 m = lds_pair(vb + L::kVMinimum + ((G * 4 + t) * 8 + g) * 8);
-    mma_f16(racc, m.x, 0u, m.y, 0u, pbh[0], pbh[1]);
-    mma_f16(racc, m.x, 0u, m.y, 0u, pbl[0], pbl[1]);
+    uint32_t m01 = mv.x, m89 = mv.y;
+    if (odd) {
+      // a row of A meets every query row: minima that are not finite are added by hand, to the rows that see
+      // them (block g, rows 2t, 2t + 1)
+      m01 &= finite_halves(m01);
+      m89 &= finite_halves(m89);
+#pragma unroll 1
+      for (int tok = 0; tok < 16; ++tok) {
+        const int from = (tok & 7) * 4 + t;
+        const float p0 = __shfl_sync(0xffffffffu, tok < 8 ? pr[0] : pr[2], from);
+        const float p1 = __shfl_sync(0xffffffffu, tok < 8 ? pr[1] : pr[3], from);
+        const uint32_t word = lds32(vb + L::kVMinimum + (((G * 4 + (tok & 7) / 2) * 8 + g) * 4 + 2 * (tok >> 3)) * 2);
+        const float x = tok & 1 ? half_hi(word) : half_lo(word);
+        if (fabsf(x) <= 65504.f) continue;
+        if (p0 != 0.f) racc[0] += x;
+        if (p1 != 0.f) racc[1] += x;
+      }
+    }
+    mma_f16(racc, m01, 0u, m89, 0u, pbh[0], pbh[1]);
+    mma_f16(racc, m01, 0u, m89, 0u, pbl[0], pbl[1]);
   }
 }
 

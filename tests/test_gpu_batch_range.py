@@ -264,6 +264,60 @@ def test_queries_with_one_loud_channel(kv_gpu, name, spread, k_fmt, v_fmt):
                 c.check(out[s], lse[s], ref, name)
 
 
+# ------------------------------------------------------------------ what is not finite
+@pytest.mark.parametrize("v_fmt", ["q4_0", "q8_0", "q4_1"])
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("group", [2, 6])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(kv_gpu, v_fmt, what, group):
+    """A value scale (or minimum) that is not finite: the rows that see its key get channels of its block that
+    are not finite, however small the key's weight is, and every other row and channel is exact."""
+    rng = np.random.default_rng(12)
+    rows, window, first = 3, 40, 300  # row i sees positions first + i - 39 .. first + i
+    T = first + rows
+    k, v, q = history(rng, T, 1.0, 0.2, 0, 1.0, group)
+    sign = np.where(rng.random(256) < 0.5, -1.0, 1.0).astype(np.float32)
+    k[first - 20] = -8 * sign  # far below every other key
+    q = (np.repeat(q, rows, 0) + sign / 4).astype(np.float32)
+    # the token before every window (its tile is read), one that only row 0 sees, the last row's own, and
+    # one of almost no weight that all rows see
+    for tokens in ([first - 40], [first - 39], [first + 2], [first - 20], [first - 40, first - 38, first + 1]):
+        for which in (0, 1) if v_fmt == "q4_1" else (0,):
+            c = History(kv_gpu, group, "q5_0" if v_fmt == "q4_1" else "q8_0", v_fmt, k, v,
+                        [(x, 3, which, what) for x in tokens])
+            clean = History(kv_gpu, group, "q5_0" if v_fmt == "q4_1" else "q8_0", v_fmt, k, v)
+            for name in ("float32", "bfloat16"):
+                qx = rounded(q, name)[0]
+                out, lse = c.batch(kv_gpu, name, qx, [first], [rows], window=window)
+                for i in range(rows):
+                    low, last = first + i - window + 1, first + i
+                    sl = slice(low, last + 1)
+                    vd = clean.held[1][sl].copy()
+                    poisoned = any(low <= x <= last for x in tokens)
+                    ref = exact_rows(qx[i], c.held[0][sl], vd)
+                    o = out[i].copy()
+                    if poisoned:
+                        assert not np.isfinite(o[:, 96:128]).any(), (tokens, i)
+                        o[:, 96:128] = ref[0][:, 96:128]
+                    check_range(o, lse[i], ref, vd, clean.codes[sl], clean.scales[sl], name, 4)
+
+
+def test_stale_slots_do_not_move_the_powers_of_two(kv_gpu):
+    """Slots past the sequence's end hold the largest scales there are: the answer is the same bits."""
+    k, v, q = history(np.random.default_rng(13), 128, 0.1, 0.05, 10, 1.0, 6)
+    tokens = 69
+    for v_fmt in ("q4_0", "q8_0", "q4_1"):
+        k_fmt = "q5_0" if v_fmt == "q4_1" else "q8_0"
+        got = []
+        for loud in (0, 1):
+            x = v.copy()
+            x[tokens:] *= 6e5 if loud and v_fmt != "q4_1" else 5e4 if loud else 1
+            x[tokens:] = np.clip(x[tokens:], -5e5, 5e5)
+            c = History(kv_gpu, 6, k_fmt, v_fmt, k, x)
+            got.append([c.batch(kv_gpu, name, rounded(q, name)[0], [tokens - 1], [1]) for name in ("float32", "bfloat16")])
+        for a, b in zip(*got):
+            assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
 # ------------------------------------------------------------- the shares of the work
 @pytest.mark.parametrize("name", ["float32", "bfloat16"])
 def test_ring_fills_over_a_pages_end(kv_gpu, name):
