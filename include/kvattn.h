@@ -192,7 +192,9 @@ KVATTN_API int kvattn_quantize_append(const kvattn_kv_desc* desc, const float* k
  * and P are split into f16 high and low parts, so the result matches exact attention over
  * the dequantized cache to about 2^-20 of sum p |v|.  The parts end 2^-37 below the row's largest
  * weight, times the larger of 1 and the largest value scale (weights), and 2^-36 below the largest
- * weight times the largest scale (their products with the scales).
+ * weight times the largest scale (their products with the scales).  A warp's sums are cut, not rounded:
+ * by up to 2^-22 for every tile of 16 keys that it adds up (a 1,776th of the tiles where the grid fills a
+ * B200 and up to 8 query rows share a KV head).
  *   ws, ws_bytes device workspace of at least kvattn_decode_workspace_size() bytes (256-byte
  *                aligned; may be NULL when that size is 0).  The keys of each KV head are
  *                split across CTAs; per-split (o, lse) partials go to the workspace and a
@@ -501,6 +503,8 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
  * Accuracy: as kvattn_decode (about 2^-20 of sum p |v|) before the output's own rounding.  Queries: fp16 rows
  * and bf16 elements within 2^-32 of their row's largest are exact, fp32 elements within 2^-17 of it keep 22
  * bits; smaller ones are held to 2^-39 of the largest.
+ * With bf16 outputs the sums are cut, not rounded: by up to 2^-22 for every tile of 16 keys that one warp (9
+ * rows and more: one group of four) adds up.
  * Supports group * max_rows <= 24 and n_seqs * H_kv * max_blocks <= 2^27 (table entries).
  * Results do not depend on timing: the split of the work depends on the lengths and the device
  * alone.  The workspace size is 0 for a batch that kvattn_decode_batch refuses. */

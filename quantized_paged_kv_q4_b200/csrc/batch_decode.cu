@@ -64,6 +64,9 @@ template <typename T>
 struct BatchParts {
   static constexpr int kQ = sizeof(T) == 4 ? 2 : 1, kTop = sizeof(T) == 4 ? 14 : 15;
   static constexpr int kSum = 6;  // block sums (zero-point keys) are 2^5 elements: divided by 2^6 they fit f16
+  // mma_parts: with bf16 outputs what the MMA cuts stays below the store's rounding (2,048 tiles in one stretch
+  // lose 2.2e-4 of the sum, half a bf16 step is 2e-3 at least), and adding tile by tile costs 2 to 8 %
+  static constexpr bool kSums = !std::is_same_v<T, __nv_bfloat16>;
 };
 
 // One unit: its n tiles start at tile t0 of its list of pages (n = 0: a sequence without rows).
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
           blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
         }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
-        attend_tile<L, KF, VF, QP, QSUM, true>(
+        attend_tile<L, KF, VF, QP, QSUM, BatchParts<T>::kSums, true>(
             kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
@@ -681,6 +684,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
   using F = TileFormat<KF, VF>;
   using L = SingleTileLayout<KF, VF>;
   constexpr int QP = BatchParts<T>::kQ, QSUM = BatchParts<T>::kSum;
+  constexpr bool SUM = BatchParts<T>::kSums;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -952,10 +956,8 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
                 uint32_t bh0, bl0, bh1, bl1;
                 scale_p<decltype(odd_tile)::value>(ph[n][0], pl[n][0], d0, bh0, bl0);
                 scale_p<decltype(odd_tile)::value>(ph[n][1], pl[n][1], d1, bh1, bl1);
-                mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
-                mma_f16(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
-                mma_f16(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
-                mma_f16(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
+                mma_parts<SUM>(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bh0, bh1, bl0, bl1);
+                mma_parts<SUM>(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bh0, bh1, bl0, bl1);
               }
               ++e;
             });
@@ -984,8 +986,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           }
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            mma_f16(racc[n], m01, 0u, m89, 0u, ph[n][0], ph[n][1]);
-            mma_f16(racc[n], m01, 0u, m89, 0u, pl[n][0], pl[n][1]);
+            mma_parts<SUM>(racc[n], m01, 0u, m89, 0u, ph[n][0], ph[n][1], pl[n][0], pl[n][1]);
           }
         }
       };

@@ -94,6 +94,23 @@ __device__ __forceinline__ void scale_p(uint32_t ph, uint32_t pl, uint32_t f, ui
   }
 }
 
+// acc += A B, B in two f16 parts.  SUM: into sums of its own first, added in fp32: the MMA cuts what does not fit
+// 24 bits of its sum, always towards zero, which a long stretch of tiles would let grow (2^-25 a step).
+template <bool SUM>
+__device__ __forceinline__ void mma_parts(float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1) {
+  if constexpr (SUM) {
+    float x[4];
+    mma_f16_z(x, a0, a1, a2, a3, bl0, bl1);
+    mma_f16(x, a0, a1, a2, a3, bh0, bh1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += x[e];
+  } else {
+    mma_f16(acc, a0, a1, a2, a3, bh0, bh1);
+    mma_f16(acc, a0, a1, a2, a3, bl0, bl1);
+  }
+}
+
 __device__ __forceinline__ uint2 lds_pair(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
@@ -398,6 +415,7 @@ __device__ __forceinline__ void tile_scale_range(uint2 d, uint2 m, bool lo, bool
 // Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
 // lane % 4; the thread's rows are 2t, 2t + 1).
 //   QP           f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
+//   SUM          whether every tile's sums are added by themselves (mma_parts)
 //   ODD          whether values that are not finite stay with the rows that see their keys, and scales that no
 //                row sees are left out of vs.  Without it every finite scale of a tile counts.
 //   qfrag(b, f)  fills f[k-step] with the query's B fragments of block b (hi0, hi1, lo0, lo1)
@@ -407,7 +425,7 @@ __device__ __forceinline__ void tile_scale_range(uint2 d, uint2 m, bool lo, bool
 //   m_run        the rows' references (above), vs the scales' state; l_run, oacc and racc are sums relative to
 //                them: of P, of P x scale x code (x vs.mul()) and of P x minimum
 // The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
-template <typename L, int KF, int VF, int QP, int QSUM, bool ODD, typename QFrag, typename Mask>
+template <typename L, int KF, int VF, int QP, int QSUM, bool SUM, bool ODD, typename QFrag, typename Mask>
 __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
                                             uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], Mask mask,
                                             ValueScale& vs, float (&m_run)[2], float (&l_run)[2],
@@ -499,10 +517,8 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
         uint32_t bh0, bl0, bh1, bl1;
         scale_p<decltype(odd_tile)::value>(pbh[0], pbl[0], hmul2(d0, mul), bh0, bl0);
         scale_p<decltype(odd_tile)::value>(pbh[1], pbl[1], hmul2(d1, mul), bh1, bl1);
-        mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1);
-        mma_f16(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bl0, bl1);
-        mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1);
-        mma_f16(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bl0, bl1);
+        mma_parts<SUM>(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1, bl0, bl1);
+        mma_parts<SUM>(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1, bl0, bl1);
       });
   };
   if (odd)
@@ -531,8 +547,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
         if (p1 != 0.f) racc[1] += x;
       }
     }
-    mma_f16(racc, m01, 0u, m89, 0u, pbh[0], pbh[1]);
-    mma_f16(racc, m01, 0u, m89, 0u, pbl[0], pbl[1]);
+    mma_parts<SUM>(racc, m01, 0u, m89, 0u, pbh[0], pbh[1], pbl[0], pbl[1]);
   }
 }
 

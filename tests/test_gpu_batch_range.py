@@ -264,6 +264,32 @@ def test_queries_with_one_loud_channel(kv_gpu, name, spread, k_fmt, v_fmt):
                 c.check(out[s], lse[s], ref, name)
 
 
+@pytest.mark.parametrize("group", [4, 20])
+def test_long_stretches_do_not_drift(kv_gpu, group):
+    """2,048 tiles in one group's stretch, values of mostly one sign.  A sum that is cut in every step is low by up
+    to 4,096 x 2^-23 of it (one unit in the last place of 24 bits a step).  Rounded tile by tile the errors are
+    independent: sqrt(2,048 / 3) steps of 2^-24 / sqrt(3) = 9e-7 of the sum, a quarter of the bound.
+    fp16: what the store rounds has no sign (the answers spread over ten steps around 1 and more): over 256 x group
+    values the mean error is within 5 x half a step / sqrt(3 x 256 x group) and that bound.
+    bf16 sums may be cut.  Their answers lie within a step or two of 1, where the steps above are twice those
+    below, so that the roundings' mean says nothing: every value by itself is within half a step and the cuts."""
+    k, v, q = history(np.random.default_rng(11), 32768, 0.5, 1.0, 0, 1.0, group)
+    c = History(kv_gpu, group, "q4_0", "q8_0", k, v)
+    for name in TYPES:
+        qx = rounded(q, name)[0]
+        ref = c.exact(qx[0])
+        out, lse = c.decode(kv_gpu, name, 12, 1, qx)
+        if name == "float32":
+            err = np.linalg.norm((out - ref[0]).reshape(12, -1), axis=1) / np.linalg.norm(ref[0])
+            assert err.max() < 2.0 ** -18, err
+        elif name == "float16":
+            drift = np.abs(((out - ref[0]) / ref[0]).reshape(12, -1).mean(1))
+            assert drift.max() < 5 * EPS[name] / (3 * 256 * group) ** 0.5 + 2.0 ** -18, drift
+        else:
+            for s in range(12):
+                c.check(out[s], lse[s], ref, name)
+
+
 # ------------------------------------------------------------------ what is not finite
 @pytest.mark.parametrize("v_fmt", ["q4_0", "q8_0", "q4_1"])
 @pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
