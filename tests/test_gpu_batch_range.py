@@ -358,6 +358,37 @@ def test_ring_fills_over_a_pages_end(kv_gpu, name):
         assert np.array_equal(first[1], again[1]) and np.array_equal(first[2], again[2])
 
 
+@pytest.mark.parametrize("group,rows", [(6, 1), (6, 4), (2, 2)])
+@pytest.mark.parametrize("how", ["whole", "window", "listed"])
+def test_more_units_than_places(kv_gpu, group, rows, how):
+    """A full server: 2,500 sequences, several to a thread of the plan and more than the grid has warp groups."""
+    rng = np.random.default_rng(14)
+    T = 420
+    k, v, q = history(rng, T, 1.0, 0.1, 0, 1.0, group)
+    c = History(kv_gpu, group, "q8_0", "q4_0", k, v)
+    S, window = 2500, 100 if how == "window" else 0
+    kinds = [(int(a), int(b)) for a, b in zip(rng.integers(0, T - rows, 12), rng.integers(0, rows + 1, 12))]
+    kinds[0], kinds[1], kinds[2] = (0, 1), (T - rows, rows), (5, 0)
+    pick = rng.integers(0, 12, S)
+    n_rows = [kinds[i][1] for i in pick]
+    for name in ("float32", "bfloat16"):
+        per_kind = rounded(rng.standard_normal((12, rows, group, 256)).astype(np.float32), name)[0]
+        qx = np.concatenate([per_kind[i, :n] for i, n in zip(pick, n_rows)])
+        out, lse = c.batch(kv_gpu, name, qx, [kinds[i][0] for i in pick], n_rows, window=window, listed=how == "listed")
+        starts = np.concatenate([[0], np.cumsum(n_rows)])
+        for i, (pos, n) in enumerate(kinds):
+            which = np.nonzero(pick == i)[0]
+            for j in range(n):
+                low = max(0, pos + j - window + 1) if window else 0
+                sl = slice(low, pos + j + 1)
+                ref = exact_rows(per_kind[i, j], c.held[0][sl], c.held[1][sl])
+                for s in which[:40]:
+                    r = starts[s] + j
+                    check_range(out[r], lse[r], ref, c.held[1][sl], c.codes[sl], c.scales[sl], name, 27)
+                # sequences that are alike get answers that differ by their cuts alone
+                assert np.abs(out[starts[which] + j] - out[starts[which[0]] + j]).max() <= (1e-5 if name == "float32" else 0.02)
+
+
 # ------------------------------------------------------------------------- tiny blocks
 @pytest.mark.parametrize("k_fmt,v_fmt", [("q4_0", "q4_0"), ("q5_0", "q4_1"), ("q8_0", "q8_0"), ("q5_1", "q4_0")])
 def test_blocks_whose_reciprocal_scale_overflows(kv_gpu, k_fmt, v_fmt):
