@@ -224,6 +224,13 @@ def _i32(x, what, device, shape):
     return _on(x, what, device)
 
 
+def _fits(what, value):
+    """A count for a 32-bit field of the C structures (ctypes would keep its low bits)."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{what}: {value} does not fit 32 bits")
+    return value
+
+
 def make_batch(row_start, pos_start, page_table, n_rows, max_rows) -> kvattn_batch:
     """The batch whose sequence s owns rows [row_start[s], row_start[s + 1]) of token arrays of
     n_rows rows, at positions pos_start[s] ..., with the pages page_table[s][h] (int32 CUDA tensors
@@ -236,7 +243,7 @@ def make_batch(row_start, pos_start, page_table, n_rows, max_rows) -> kvattn_bat
     b = kvattn_batch(_i32(row_start, "row_start", device, (n_seqs + 1,)),
                      _i32(pos_start, "pos_start", device, (n_seqs,)),
                      _i32(page_table, "page_table", device, (n_seqs, heads, max_blocks)),
-                     n_rows, n_seqs, max_rows, max_blocks, 0)
+                     n_rows, n_seqs, _fits("max_rows", max_rows), max_blocks, 0)
     b.heads, b.device = heads, device
     return b
 
@@ -442,6 +449,7 @@ def kvattn_decode_batch_workspace_size(desc, batch) -> int:
 def kvattn_decode_batch(desc, batch, q, out, lse, ws, page_logical=None, n_pages=None, window=0, stream=None) -> None:
     """Attention of every row of the batch over its sequence's pages: q, out [n_rows][H_q][256] of one
     type, lse fp32 [n_rows][H_q], ws a tensor of at least kvattn_decode_batch_workspace_size bytes."""
+    _fits("window", window)
     device = _check_batch("kvattn_decode_batch", desc, batch)
     n, heads, q_heads = batch.n_rows, batch.heads, desc.n_q_heads
     if lse.dtype is not _torch().float32 or lse.shape != (n, q_heads):

@@ -23,3 +23,21 @@ def test_no_workspace_for_a_batch_that_decode_refuses(lib, kw):
 def test_a_batch_without_rows_is_fine_whatever_its_table(lib):
     assert lib.kvattn_decode_batch(desc(), batch(n_rows=0, n_seqs=1 << 13, max_blocks=(1 << 12) + 1), None, None, None, 0,
                                    None, None, None, 0, None) == kvattn.OK
+
+
+def test_counts_that_do_not_fit_are_refused(monkeypatch):
+    """A window of 2^32 + 5 is not a window of 5."""
+    import torch
+
+    b = batch()
+    b.heads, b.device = 4, 0
+    for window in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="window"):
+            kvattn.kvattn_decode_batch(desc(), b, None, None, None, None, window=window)
+    monkeypatch.setattr(kvattn, "_on", lambda x, what, device: x.data_ptr())
+    monkeypatch.setattr(kvattn._Torch, "current_device", lambda: 0)
+    monkeypatch.setattr(kvattn._Torch, "int32", torch.int32)
+    row, pos, table = (torch.zeros(s, dtype=torch.int32) for s in ((3,), (2,), (2, 4, 5)))
+    assert kvattn.make_batch(row, pos, table, 10, 2 ** 31 - 1).max_rows == 2 ** 31 - 1
+    with pytest.raises(ValueError, match="max_rows"):
+        kvattn.make_batch(row, pos, table, 10, 2 ** 32 + 1)
