@@ -489,8 +489,10 @@ KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch*
  * past fp16's range) reaches the rows that see its key, in the channels of its block, and no other.
  *   q            [n_rows][H_q][256]
  *   page_logical device int32 [n_seqs][H_kv][max_blocks]: the logical block of each entry of
- *                page_table, which then is a list of pages in any order (a selection of
- *                kvattn_select_blocks over n_seqs * H_kv units); NULL: entry i is block i
+ *                page_table, which then is a list of pages in any order, none of them twice; NULL:
+ *                entry i is block i.  kvattn_select_blocks fills such lists (sel_phys, sel_logical and
+ *                n_sel with cap = max_blocks): its units are (sequence, KV head), and as it takes one
+ *                length for all of them, sequences of different lengths take a call each, of H_kv units
  *   n_pages      device int32 [n_seqs][H_kv]: entries in use (clamped to [0, max_blocks]);
  *                NULL without page_logical: as many as the sequence has blocks; NULL with it:
  *                max_blocks

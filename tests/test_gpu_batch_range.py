@@ -1,5 +1,6 @@
-"""GPU: the ragged-batch decode where its numbers and its work get uneven: rings that fill over a page's
-end, more units than the grid has places."""
+"""GPU: the ragged-batch decode where its numbers and its work get uneven: dominant keys, tiny and huge values,
+values that are not finite, long stretches, rings that fill over a page's end, more units than the grid has
+places, and lists that the selection fills."""
 import numpy as np
 import pytest
 
@@ -422,3 +423,36 @@ def test_blocks_whose_reciprocal_scale_overflows(kv_gpu, k_fmt, v_fmt):
         for a, b in zip(got["tiny"], got["clean"]):
             assert np.array_equal(a, b)
     assert kv.kvattn_device_error() == 0
+
+
+# ------------------------------------------------------------------- selection, then attention
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+def test_selected_blocks_of_sequences_of_different_lengths(kv_gpu, name):
+    """Summaries and a selection per sequence, each into its own rows of the lists, and one attention call."""
+    import torch
+
+    kv = kv_gpu
+    H, group, budget, recent, cap = 2, 6, 3, 1, 6
+    c = BatchCache([(1500, 2), (700, 1), (300, 3)], H, group, "q8_0", "q4_0", 64).on_gpu(kv)
+    rng = np.random.default_rng(16)
+    qx = rounded(rng.standard_normal((c.total, H * group, 256)).astype(np.float32), name)[0]
+    q = torch.from_numpy(qx).to(getattr(torch, name)).cuda()
+    logical, phys = (torch.full((3, H, cap), -5, dtype=torch.int32, device="cuda") for _ in range(2))
+    n = torch.zeros((3, H), dtype=torch.int32, device="cuda")
+    ws = torch.empty(kv.kvattn_select_workspace_size(H, c.blocks), dtype=torch.uint8, device="cuda")
+    for s, (ctx, rows) in enumerate(c.lens):
+        full, total = (ctx + rows) // 128, (ctx + rows + 127) // 128
+        summaries = torch.zeros((H, c.blocks, 256), device="cuda")
+        table = c.t_table[s].contiguous()
+        kv.kvattn_block_summaries(c.desc, table, H, c.blocks, 0, full, summaries)
+        ask = q[int(c.row_start[s])].float().view(H, group, 256).contiguous()
+        kv.kvattn_select_blocks(summaries, ask, H, group, c.blocks, full, total, budget, recent, table, logical[s],
+                                phys[s], n[s], cap, ws, ws.nbytes)
+    batch = kv.make_batch(c.t_row, c.t_pos, phys, c.total, c.max_rows)
+    out, lse = torch.zeros_like(q), torch.zeros((c.total, H * group), device="cuda")
+    dws = torch.empty(kv.kvattn_decode_batch_workspace_size(c.desc, batch), dtype=torch.uint8, device="cuda")
+    kv.kvattn_decode_batch(c.desc, batch, q, out, lse, dws, page_logical=logical, n_pages=n)
+    assert kv.kvattn_device_error() == 0
+    log, counts = logical.cpu().numpy(), n.cpu().numpy()
+    assert (counts == np.array([[5], [5], [3]])).all()  # budget, the recent block and the tail; 300 + 3 tokens: all
+    check_decode(c, name, qx, out.float().cpu().numpy(), lse.cpu().numpy(), listed=lambda s, h: log[s, h, :counts[s, h]])
