@@ -477,7 +477,7 @@ KVATTN_API int kvattn_append_batch(const kvattn_kv_desc* desc, const kvattn_batc
 /* Writes the values that the cache holds for every row of the batch: code x scale (+ minimum),
  * rounded to fp32 (exact without a minimum) and then to the output's type.  A row whose page
  * id is out of range is written as zeros (and recorded).  k or v may be NULL: that side is
- * then neither read nor written.
+ * then neither read nor written.  The two arrays must not overlap.
  *   k, v   [n_rows][H_kv][256], of one dtype */
 KVATTN_API int kvattn_read_batch(const kvattn_kv_desc* desc, const kvattn_batch* batch, const kvattn_rows* k,
                                  const kvattn_rows* v, kvattn_stream_t stream);

@@ -456,3 +456,40 @@ def test_selected_blocks_of_sequences_of_different_lengths(kv_gpu, name):
     log, counts = logical.cpu().numpy(), n.cpu().numpy()
     assert (counts == np.array([[5], [5], [3]])).all()  # budget, the recent block and the tail; 300 + 3 tokens: all
     check_decode(c, name, qx, out.float().cpu().numpy(), lse.cpu().numpy(), listed=lambda s, h: log[s, h, :counts[s, h]])
+
+
+# ----------------------------------------------------------------- inputs that are not finite
+@pytest.mark.parametrize("k_fmt,v_fmt", PAIRS)
+def test_inputs_that_are_not_finite_are_written_as_by_the_single_sequence_call(kv_gpu, k_fmt, v_fmt):
+    """NaN and infinities, alone and together, in some blocks: the same bytes from both writers, and every other
+    block's are those of clean rows."""
+    import torch
+
+    kv = kv_gpu
+    rng = np.random.default_rng(17)
+    for rows in (16, 5):
+        x = rng.standard_normal((rows, 1, 256)).astype(np.float32)
+        clean = x.copy()
+        for i in range(rows):
+            block = 32 * (i % 8)
+            for j, what in enumerate((np.nan, np.inf, -np.inf)):
+                if (i + 1) >> j & 1:
+                    x[i, 0, block + rng.choice(32, 2, replace=False)] = what
+            clean[i, 0, block:block + 32] = 0
+        back = {}
+        for what, data in (("odd", x), ("clean", clean)):
+            c = BatchCache([(0, rows)], 1, 1, k_fmt, v_fmt, 63, written="before", fill=0).on_gpu(kv)
+            t = torch.from_numpy(data).cuda()
+            kv.kvattn_append_batch(c.desc, c.batch, t, t)
+            k2, v2 = torch.zeros_like(c.k_pool), torch.zeros_like(c.v_pool)
+            d2 = kv.make_desc(1, 1, k2, v2, c.n_phys, k_fmt=k_fmt, v_fmt=v_fmt)
+            kv.kvattn_quantize_append(d2, t, t, rows, 0, c.t_table[0].contiguous(), c.blocks)
+            assert torch.equal(k2, c.k_pool) and torch.equal(v2, c.v_pool), what
+            back[what] = [torch.zeros((rows, 1, 256), device="cuda") for _ in range(2)]
+            kv.kvattn_read_batch(c.desc, c.batch, *back[what])
+        for a, b in zip(back["odd"], back["clean"]):
+            for i in range(rows):
+                keep = np.ones(256, bool)
+                keep[32 * (i % 8):32 * (i % 8) + 32] = False
+                assert np.array_equal(a.cpu().numpy()[i, 0, keep], b.cpu().numpy()[i, 0, keep])
+    assert kv.kvattn_device_error() == 0
