@@ -106,13 +106,14 @@ struct BatchCfg {
   static constexpr int kRowsPad = 8;
   static constexpr int kTileBytes = L::kBytes;
   static constexpr int kQBytes = BatchParts<T>::kQ * 8 * 32 * 16;  // the query's B fragments (load_qfrag)
-  static constexpr int kFit = kBatchRoom / (kQBytes + 2 * kTileBytes);
+  static constexpr int kFixed = kQBytes + 256;                     // and a tile's lifted value scales
+  static constexpr int kFit = kBatchRoom / (kFixed + 2 * kTileBytes);
   static constexpr int kGroups = kFit < 12 ? kFit : 12;
-  static constexpr int kStagesFit = (kBatchRoom / kGroups - kQBytes) / kTileBytes;
+  static constexpr int kStagesFit = (kBatchRoom / kGroups - kFixed) / kTileBytes;
   static constexpr int kStages = kStagesFit < 6 ? kStagesFit : 6;
   static constexpr int kWarps = kGroups;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kGroupBytes = kStages * kTileBytes + kQBytes;
+  static constexpr int kGroupBytes = kStages * kTileBytes + kFixed;
   static constexpr int kMetaOff = kGroups * kGroupBytes;
   static constexpr int kSmemBytes = kMetaOff + kBatchMeta;
   static_assert(kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
@@ -123,13 +124,16 @@ struct BatchCfg {
   static constexpr int kUnitCost = 4, kMinShare = 2;
 };
 
+constexpr uint32_t kBlind = 1u << 31;  // some row sees a value of the tile that is not finite
+
 // The wide kernel's state of a unit, per group: rows in order.
 template <int NR>
 struct alignas(16) WideState {
   float crow[8 * NR];
   int qpos[8 * NR];
   float top[4][8 * NR], sum[4][8 * NR];  // of each warp
-  uint32_t seen[4], all[4];              // of each warp's tile (tile_scale_range)
+  uint32_t most[4];                      // the largest scale of each warp's tile (and kBlind)
+  uint32_t blind[4][8 * NR];             // blind_blocks of each warp's tile
   uint2 qsums[NR][32];                   // zero-point keys: block sums as B fragments
 };
 
@@ -200,24 +204,6 @@ __device__ __forceinline__ BatchUnit next_unit(const BatchDecodeParams& p, int u
     if (w.n > 0) return w;
     u = (u / p.b.n_kv + 1) * p.b.n_kv - 1;  // a sequence without rows: none of its heads has any
   }
-}
-
-// Zeroes the V scales (and minima) of the tokens of a staged tile that lie past the sequence's
-// last position: their bytes are whatever the page held, and 0 x NaN would reach the output.
-// One lane per (T, block) word of four tokens.
-__device__ __noinline__ void blank_tokens(uint8_t* vscale, uint8_t* vmin, int lane, int n_live) {
-  const int T = lane >> 3;
-  uint32_t keep[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w)
-    keep[w] = (2 * T + 8 * w < n_live ? 0x0000FFFFu : 0u) | (2 * T + 1 + 8 * w < n_live ? 0xFFFF0000u : 0u);
-  uint2* a = reinterpret_cast<uint2*>(vscale) + lane;
-  *a = make_uint2(a->x & keep[0], a->y & keep[1]);
-  if (vmin) {
-    uint2* m = reinterpret_cast<uint2*>(vmin) + lane;
-    *m = make_uint2(m->x & keep[0], m->y & keep[1]);
-  }
-  __syncwarp();
 }
 
 __device__ __forceinline__ const uint8_t* lds_ptr(const uint8_t* const* p) {
@@ -585,13 +571,9 @@ __global__ void __launch_bounds__(BatchCfg<KF, VF, T>::kThreads, 1) decode_batch
       const int key = *reinterpret_cast<volatile int*>(&key_of[st]);
       if (key >= 0) {
         const uint32_t kb = ring_s + st * C::kTileBytes;
-        if (key + 15 > last) {
-          uint8_t* vs = ring + st * C::kTileBytes + L::kV + L::kVScale;
-          blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
-        }
         const bool need_mask = key + 15 > un.pos0 || key <= last - span;
         attend_tile<L, KF, VF, QP, QSUM, BatchParts<T>::kSums, true>(
-            kb, kb + L::kV, 0, g, t, qfrag, qsb_hi, qsb_lo, crow,
+            kb, kb + L::kV, q_s + C::kQBytes, 0, g, t, qfrag, qsb_hi, qsb_lo, crow,
             [&](int e, float x) {
               const int at = key + g + 8 * (e >> 1);
               return need_mask && (at > qpos[e & 1] || at <= qpos[e & 1] - span) ? -INFINITY : x;
@@ -703,7 +685,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
   uint8_t* ring = smem + grp * C::kGroupBytes;
   const uint32_t ring_s = smem_u32(ring), q_s = ring_s + C::kStages * C::kStepBytes;
   const uint32_t p_s = q_s + NR * C::kQTileBytes;
-  auto* state = reinterpret_cast<WideState<NR>*>(ring + C::kStages * C::kStepBytes + NR * C::kQTileBytes + 4 * C::kPTileBytes);
+  auto* state = reinterpret_cast<WideState<NR>*>(ring + C::kGroupBytes - sizeof(WideState<NR>));
   Producer* prod = &plan->producer[warp];
   auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory"); };
 
@@ -817,14 +799,10 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       const uint32_t kb = ring_s + st * C::kStepBytes + w * C::kTileBytes;
       const bool live = k + w < end && key >= 0;
       float sv[NR][4];
-      uint2 dv = make_uint2(0u, 0u), mv = make_uint2(0u, 0u);  // scales and minima of block g, tokens 2t, + 1, + 8, + 9
+      TileScales ts;
+      ts.d = make_uint2(0u, 0u);
       if (live) {
-        if (key + 15 > last) {
-          uint8_t* vs = ring + st * C::kStepBytes + w * C::kTileBytes + L::kV + L::kVScale;
-          blank_tokens(vs, F::kVMin ? vs + (L::kVMinimum - L::kVScale) : nullptr, lane, last - key + 1);
-        }
-        dv = lds_pair(kb + L::kV + L::kVScale + (t * 8 + g) * 8);
-        if constexpr (F::kVMin) mv = lds_pair(kb + L::kV + L::kVMinimum + (t * 8 + g) * 8);
+        ts.load<L, F::kVMin>(kb + L::kV, 0, g, t);
         tile_scores<L, KF, VF, QP, QSUM, NR>(
             kb, 0, g, t,
             [&](int n, int bl, uint4 (&f)[2]) { load_qfrag<QP>(q_s + n * C::kQTileBytes, bl, lane, f); },
@@ -850,8 +828,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           for (int e = 0; e < 4; ++e) sv[n][e] = -INFINITY;
       }
       // ---- the rows' references and the scales' powers of two, as in the one-warp kernel
-      uint32_t need = exceeds(dv.x, dv.y, vs.bound);
-      if constexpr (F::kVMin) need |= exceeds(mv.x, mv.y, 0x7BFF7BFFu);
+      uint32_t need = ts.unusual<F::kVMin>(vs);
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -866,17 +843,24 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           : "memory");
       // every warp is done with the step before this one: its stage takes the step S - 1 ahead
       issue((step + C::kStages - 1) % C::kStages);
-      bool odd = false;
       if (need) {
-        {
-          bool lo = false, hi = false;
+        bool lo = false, hi = false;
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) lo |= sv[n][c] != -INFINITY, hi |= sv[n][c + 2] != -INFINITY;
-          uint32_t seen, all;
-          tile_scale_range<true>(dv, mv, lo, hi, t, &seen, &all);
-          if (lane == 0) state->seen[w] = seen, state->all[w] = all;
+          for (int c = 0; c < 2; ++c) lo |= sv[n][c] != -INFINITY, hi |= sv[n][c + 2] != -INFINITY;
+        uint32_t most;
+        const uint32_t bad = ts.clean(lo, hi, t, &most);
+        if (live) ts.store<L, F::kVMin>(kb + L::kV, 0, g, t);  // (behind the next barriers all read them)
+        const bool any = __any_sync(0xffffffffu, bad != 0);
+        if (lane == 0) state->most[w] = most | (any ? kBlind : 0u);
+        if (any) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            uint32_t blind[2] = {0u, 0u};
+            blind_blocks(bad, sv[n], t, blind);
+            if (g == 0) state->blind[w][8 * n + 2 * t] = blind[0], state->blind[w][8 * n + 2 * t + 1] = blind[1];
+          }
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -889,12 +873,28 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
             if (g == 0) state->top[w][8 * n + 2 * t + c] = mx;
           }
         group_sync();
-        const uint4 seen = lds128(smem_u32(state->seen)), all = lds128(smem_u32(state->all));
+        const uint4 tops = lds128(smem_u32(state->most));
+        const uint32_t top4[4] = {tops.x, tops.y, tops.z, tops.w};
+        if ((tops.x | tops.y | tops.z | tops.w) & kBlind) {
+#pragma unroll 1
+          for (int u = 0; u < 4; ++u) {
+            if (!(state->most[u] & kBlind)) continue;
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (state->blind[u][8 * n + 2 * t + (e & 1)] >> (8 * w + 4 * (i >> 1)) & 1u) oacc[i][n][e] = NAN;
+          }
+        }
+        uint32_t most_of_all = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) most_of_all = max(most_of_all, top4[u] & ~kBlind);
         const float top = vs.top;
         int dk;
         float ratio;
-        vs.raise(max(max(seen.x, seen.y), max(seen.z, seen.w)), &dk, &ratio);
-        odd = max(max(all.x, all.y), max(all.z, all.w)) > (vs.bound & 0xFFFFu);
+        vs.raise(most_of_all, &dk, &ratio);
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -925,10 +925,6 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
           pr[c + 2] = fast_exp2(sv[n][c + 2] - mu);
           l_run[n][c] += pr[c] + pr[c + 2];
         }
-        if (odd) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pr[e] = seen_p(pr[e], sv[n][e]);
-        }
         uint32_t h01, l01, h23, l23;
         split_pair(pr[0], pr[1], h01, l01);
         split_pair(pr[2], pr[3], h23, l23);
@@ -938,7 +934,7 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       group_sync();
       // ---- O^T += V^T P^T for this warp's channels, over the step's tiles
       const uint32_t mul = vs.mul();
-      auto add_values = [&](int u, auto odd_tile) {
+      auto add_values = [&](int u) {
         const uint32_t vb = ring_s + st * C::kStepBytes + u * C::kTileBytes + L::kV;
         uint32_t ph[NR][2], pl[NR][2];
 #pragma unroll
@@ -948,45 +944,25 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
         }
         int e = 0;  // constant in the unrolled code
         tile_value_pair<L, KF, VF>(
-            vb, 0, w, g, t, [&](int, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
+            vb, vb + L::kVScale, 0, w, g, t,
+            [&](int, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
               d0 = hmul2(d0, mul);
               d1 = hmul2(d1, mul);
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
                 uint32_t bh0, bl0, bh1, bl1;
-                scale_p<decltype(odd_tile)::value>(ph[n][0], pl[n][0], d0, bh0, bl0);
-                scale_p<decltype(odd_tile)::value>(ph[n][1], pl[n][1], d1, bh1, bl1);
+                split_scaled(ph[n][0], pl[n][0], d0, bh0, bl0);
+                split_scaled(ph[n][1], pl[n][1], d1, bh1, bl1);
                 mma_parts<SUM>(oacc[2 * e][n], a0[0], a0[1], a0[2], a0[3], bh0, bh1, bl0, bl1);
                 mma_parts<SUM>(oacc[2 * e + 1][n], a1[0], a1[1], a1[2], a1[3], bh0, bh1, bl0, bl1);
               }
               ++e;
             });
         if constexpr (F::kVMin) {
-          const uint2 mw = lds_pair(vb + L::kVMinimum + (t * 8 + g) * 8);
-          uint32_t m01 = mw.x, m89 = mw.y;
-          if constexpr (decltype(odd_tile)::value) {
-            // minima that are not finite, by hand (attend_tile): block g, rows 8n + 2t (+ 1); P of a
-            // row and token sits with lane (row, token / 2 % 4)
-            m01 &= finite_halves(m01);
-            m89 &= finite_halves(m89);
-#pragma unroll 1
-            for (int tok = 0; tok < 16; ++tok) {
-              const uint32_t word = lds32(vb + L::kVMinimum + (((tok & 7) / 2 * 8 + g) * 4 + 2 * (tok >> 3)) * 2);
-              const float x = tok & 1 ? half_hi(word) : half_lo(word);
-              if (fabsf(x) <= 65504.f) continue;
-#pragma unroll
-              for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const uint32_t pw = lds32(p_s + u * C::kPTileBytes +
-                                            (n * 32 + (2 * t + c) * 4 + (tok & 7) / 2) * C::kPFragBytes + 4 * (tok >> 3));
-                  if ((tok & 1 ? pw >> 16 : pw) & 0x7FFFu) racc[n][c] += x;
-                }
-            }
-          }
+          const uint2 m = lds_pair(vb + L::kVMinimum + (t * 8 + g) * 8);
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            mma_parts<SUM>(racc[n], m01, 0u, m89, 0u, ph[n][0], ph[n][1], pl[n][0], pl[n][1]);
+            mma_parts<SUM>(racc[n], m.x, 0u, m.y, 0u, ph[n][0], ph[n][1], pl[n][0], pl[n][1]);
           }
         }
       };
@@ -994,18 +970,14 @@ __global__ void __launch_bounds__(WideCfg<KF, VF, NR, T>::kThreads, 1)
       asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(keys.x), "=r"(keys.y), "=r"(keys.z), "=r"(keys.w)
                    : "r"(smem_u32(key_of + 4 * st)));
-      if (odd) {
-#pragma unroll 1
-        for (int u = 0; u < 4 && k + u < end; ++u)
-          if (lds_int(&key_of[4 * st + u]) >= 0) add_values(u, std::true_type{});
-      } else if (k + 4 <= end && (keys.x | keys.y | keys.z | keys.w) >= 0) {
+      if (k + 4 <= end && (keys.x | keys.y | keys.z | keys.w) >= 0) {
         // all four are there: their loads and decoding overlap
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add_values(u, std::false_type{});
+        for (int u = 0; u < 4; ++u) add_values(u);
       } else {
 #pragma unroll 1
         for (int u = 0; u < 4 && k + u < end; ++u)
-          if (lds_int(&key_of[4 * st + u]) >= 0) add_values(u, std::false_type{});
+          if (lds_int(&key_of[4 * st + u]) >= 0) add_values(u);
       }
     }
     k = end;

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(DecodeCfg<KF, VF, NT>::kThreads, 1) decode_ker
           }
           const int key0 = logical * kPageTokens + 16 * G + g;  // rows e<2: token g, e>=2: g+8
           attend_tile<PageLayout<KF, VF>, KF, VF, 2, 0, false, false>(
-              kb, vb, G, g, t, qfrag, qsb_hi, qsb_lo, crow,
+              kb, vb, 0u, G, g, t, qfrag, qsb_hi, qsb_lo, crow,
               [&](int e, float x) {
                 return need_mask && key0 + 8 * (e >> 1) > qpos_row[e & 1] ? -INFINITY : x;
               },

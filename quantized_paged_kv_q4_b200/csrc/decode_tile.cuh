@@ -2,8 +2,6 @@
 // arithmetic, which the single-sequence and the ragged-batch decode share.
 #pragma once
 
-#include <type_traits>
-
 #include "common.cuh"
 
 namespace kvattn {
@@ -68,34 +66,8 @@ __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uin
   lo = pack_half2(x0 - half_lo(hi), x1 - half_hi(hi));
 }
 
-// 0xFFFF in each half of x that is not zero / that is finite.
-__device__ __forceinline__ uint32_t nonzero_halves(uint32_t x) {
-  return ((x & 0x7FFFu) ? 0x0000FFFFu : 0u) | ((x & 0x7FFF0000u) ? 0xFFFF0000u : 0u);
-}
-__device__ __forceinline__ uint32_t finite_halves(uint32_t x) {
-  return ((x & 0x7C00u) != 0x7C00u ? 0x0000FFFFu : 0u) | ((x & 0x7C000000u) != 0x7C000000u ? 0xFFFF0000u : 0u);
-}
-
-// P of a key in a tile of odd scales: never 0 where the row sees the key (2^-24 is f16's smallest step), so
-// that a value which is not finite stays one, however small its weight.
-__device__ __forceinline__ float seen_p(float p, float score) {
-  return p < 0x1p-24f && score != -INFINITY ? 0x1p-24f : p;
-}
-
-// P (its f16 parts) times the per-token scales f of a block.  ODD: f may hold what is not finite, which
-// reaches the rows that see its key (P is not zero) and no other.
-template <bool ODD>
-__device__ __forceinline__ void scale_p(uint32_t ph, uint32_t pl, uint32_t f, uint32_t& hi, uint32_t& lo) {
-  split_scaled(ph, pl, f, hi, lo);
-  if constexpr (ODD) {
-    const uint32_t keep = nonzero_halves(ph);
-    hi &= keep;
-    lo &= keep;
-  }
-}
-
 // acc += A B, B in two f16 parts.  SUM: into sums of its own first, added in fp32: the MMA cuts what does not fit
-// 24 bits of its sum, always towards zero, which a long stretch of tiles would let grow (2^-25 a step).
+// 24 bits of its sum, always towards zero, which a long stretch of tiles lets grow (about 2^-24 of the sum a step).
 template <bool SUM>
 __device__ __forceinline__ void mma_parts(float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1) {
@@ -109,6 +81,10 @@ __device__ __forceinline__ void mma_parts(float (&acc)[4], uint32_t a0, uint32_t
     mma_f16(acc, a0, a1, a2, a3, bh0, bh1);
     mma_f16(acc, a0, a1, a2, a3, bl0, bl1);
   }
+}
+
+__device__ __forceinline__ void sts_pair(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
 __device__ __forceinline__ uint2 lds_pair(uint32_t addr) {
@@ -289,14 +265,14 @@ __device__ __forceinline__ void tile_scores(uint32_t kb, int G, int g, int t, QF
 }
 
 // The codes of value blocks 2C and 2C + 1 of one tile as A fragments (16 dims x 16 tokens, exact in f16):
-// f(block, dims 0-15, dims 16-31, scales of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9).
+// f(block, dims 0-15, dims 16-31, scales of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9).  The scales are those at
+// `scales`, the tile's own or its lifted copy.
 template <typename L, int KF, int VF, typename Use>
-__device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g, int t, Use f) {
+__device__ __forceinline__ void tile_value_pair(uint32_t vb, uint32_t scales, int G, int C, int g, int t, Use f) {
   using F = TileFormat<KF, VF>;
   if constexpr (VF != kValQ8) {
     const uint4 vw = lds128(vb + ((((G * 4 + C) * 8 + g) * 4 + t) * 16));
-    const uint32_t sidx = vb + L::kVScale + (((G * 4 + t) * 8 + 2 * C) * 4) * 2;
-    const uint4 dv = lds128(sidx);
+    const uint4 dv = lds128(scales + (t * 8 + 2 * C) * 8);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint32_t W0 = e ? vw.z : vw.x, W1 = e ? vw.w : vw.y;
@@ -319,10 +295,7 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g
     for (int e = 0; e < 2; ++e) {
       const int b = 2 * C + e;
       const uint4 vw = lds128(vb + ((((G * 8 + b) * 8 + g) * 4 + t) * 16));
-      uint32_t d0, d1;
-      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                   : "=r"(d0), "=r"(d1)
-                   : "r"(vb + L::kVScale + (((G * 4 + t) * 8 + b) * 4) * 2));
+      const uint2 dv = lds_pair(scales + (t * 8 + b) * 8);
       const uint32_t w[4] = {vw.x, vw.y, vw.z, vw.w};  // offset-binary code bytes (q + 128)
       uint32_t a[2][4];
 #pragma unroll
@@ -330,7 +303,7 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, int G, int C, int g
         a[q >> 1][2 * (q & 1)] = hsub2(prmt(w[q], kByte64x4, 0x4140u), kHalf2_1152);
         a[q >> 1][2 * (q & 1) + 1] = hsub2(prmt(w[q], kByte64x4, 0x4342u), kHalf2_1152);
       }
-      f(b, a[0], a[1], d0, d1);
+      f(b, a[0], a[1], dv.x, dv.y);
     }
   }
 }
@@ -383,41 +356,91 @@ __device__ __forceinline__ bool exceeds(uint32_t a, uint32_t b, uint32_t bound) 
   return over != 0;
 }
 
-// The largest scale of a tile, as f16 bits, among the keys that some row sees and that are finite (*seen), and
-// among all (*all: 0xFFFF with a NaN or an infinity, of a minimum too).  Lane (g, t) holds the scales (and
-// minima) of block g, tokens 2t, 2t + 1 in the first word and 2t + 8, 2t + 9 in the second; lo and hi
-// say whether a row of the lane's sees token g, g + 8 (mma.sync's accumulator layout).
-template <bool ODD>
-__device__ __forceinline__ void tile_scale_range(uint2 d, uint2 m, bool lo, bool hi, int t, uint32_t* seen,
-                                                 uint32_t* all) {
-  uint32_t vis[2] = {0u, 0u};
-  if constexpr (ODD) {
-    vis[0] = __ballot_sync(0xffffffffu, lo);
-    vis[1] = __ballot_sync(0xffffffffu, hi);
+// The scales (and minima) of one tile's values as lane (g, t) holds them: block g, tokens 2t, 2t + 1 in the first
+// word, 2t + 8, 2t + 9 in the second.
+struct TileScales {
+  uint2 d, m = {0u, 0u};
+  template <typename L, bool VMIN>
+  __device__ __forceinline__ void load(uint32_t vb, int G, int g, int t) {
+    const uint32_t at = vb + L::kVScale + ((G * 4 + t) * 8 + g) * 8;
+    d = lds_pair(at);
+    if constexpr (VMIN) m = lds_pair(at + (L::kVMinimum - L::kVScale));
   }
-  const uint32_t w[2] = {d.x, d.y}, n[2] = {m.x, m.y};
-  uint32_t s = 0, a = 0;
+  template <typename L, bool VMIN>
+  __device__ __forceinline__ void store(uint32_t vb, int G, int g, int t) const {
+    const uint32_t at = vb + L::kVScale + ((G * 4 + t) * 8 + g) * 8;
+    sts_pair(at, d.x, d.y);
+    if constexpr (VMIN) sts_pair(at + (L::kVMinimum - L::kVScale), m.x, m.y);
+  }
+  // whether the powers of two have to move, or something here is not finite
+  template <bool VMIN>
+  __device__ __forceinline__ bool unusual(const ValueScale& vs) const {
+    bool x = exceeds(d.x, d.y, vs.bound);
+    if constexpr (VMIN) x |= exceeds(m.x, m.y, 0x7BFF7BFFu);
+    return x;
+  }
+  // Zeroes what no row sees (whatever it is) and what is not finite.  lo and hi: whether a row of the lane's sees
+  // token g, g + 8 (mma.sync's accumulator layout).  *most: the largest scale left in the tile, as f16 bits.
+  // Returns the lane's tokens that some row sees and that are not finite: bit 2H + i for token 2t + i + 8H.
+  __device__ __forceinline__ uint32_t clean(bool lo, bool hi, int t, uint32_t* most) {
+    const uint32_t vis[2] = {__ballot_sync(0xffffffffu, lo), __ballot_sync(0xffffffffu, hi)};
+    uint32_t w[2] = {d.x, d.y}, n[2] = {m.x, m.y}, bad = 0, top = 0;
 #pragma unroll
-  for (int H = 0; H < 2; ++H)
-#pragma unroll
-    for (int odd = 0; odd < 2; ++odd) {
-      uint32_t x = (w[H] >> (16 * odd)) & 0x7FFFu;
-      const uint32_t y = (n[H] >> (16 * odd)) & 0x7FFFu;
-      const bool live = !ODD || ((vis[H] >> (8 * t + 4 * odd)) & 15u);
-      if (x < 0x7C00u && live) s = max(s, x);
-      if (x >= 0x7C00u || y >= 0x7C00u) x = 0xFFFFu;
-      a = max(a, x);
+    for (int j = 0; j < 4; ++j) {
+      const int H = j >> 1, i = j & 1;
+      const uint32_t half = 0xFFFFu << (16 * i), inf = 0x7C00u << (16 * i);
+      const bool seen = (vis[H] >> (8 * t + 4 * i)) & 15u, finite = (w[H] & inf) != inf && (n[H] & inf) != inf;
+      if (seen && !finite) bad |= 1u << j;
+      if (!seen || !finite) w[H] &= ~half, n[H] &= ~half;
+      top = max(top, (w[H] >> (16 * i)) & 0x7FFFu);
     }
-  *seen = __reduce_max_sync(0xffffffffu, s);
-  *all = ODD ? __reduce_max_sync(0xffffffffu, a) : 0u;
+    d = make_uint2(w[0], w[1]);
+    m = make_uint2(n[0], n[1]);
+    *most = __reduce_max_sync(0xffffffffu, top);
+    return bad;
+  }
+  // The largest finite scale of the tile, whoever sees it.
+  __device__ __forceinline__ uint32_t largest() const {
+    const uint32_t w[2] = {d.x, d.y};
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = (w[j >> 1] >> (16 * (j & 1))) & 0x7FFFu;
+      if (x < 0x7C00u) top = max(top, x);
+    }
+    return __reduce_max_sync(0xffffffffu, top);
+  }
+  // The lifted scales, into the tile's copy.
+  __device__ __forceinline__ void lift(const ValueScale& vs, uint32_t scales, int g, int t) const {
+    const uint32_t mul = vs.mul();
+    sts_pair(scales + (t * 8 + g) * 8, hmul2(d.x, mul), hmul2(d.y, mul));
+  }
+};
+
+// Bit 4b of rows[c]: row 2t + c sees a key whose block b is not finite.  bad: TileScales::clean of every lane; sv:
+// the rows' scores, -inf where a key is unseen.
+__device__ __forceinline__ void blind_blocks(uint32_t bad, const float (&sv)[4], int t, uint32_t (&rows)[2]) {
+  const uint32_t b0 = __ballot_sync(0xffffffffu, bad & 1u), b1 = __ballot_sync(0xffffffffu, bad & 2u);
+  const uint32_t b2 = __ballot_sync(0xffffffffu, bad & 4u), b3 = __ballot_sync(0xffffffffu, bad & 8u);
+#pragma unroll 1
+  for (int tok = 0; tok < 16; ++tok) {
+    const uint32_t of = tok < 8 ? (tok & 1 ? b1 : b0) : (tok & 1 ? b3 : b2);
+    const uint32_t blocks = (of >> ((tok & 7) >> 1)) & 0x11111111u;
+    const int from = (tok & 7) * 4 + t;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (__shfl_sync(0xffffffffu, tok < 8 ? sv[c] : sv[2 + c], from) != -INFINITY) rows[c] |= blocks;
+  }
 }
 
 // Adds one tile of 16 tokens to the online softmax of 8 query rows (one warp; g = lane / 4, t =
 // lane % 4; the thread's rows are 2t, 2t + 1).
 //   QP           f16 parts of the query: 2 keeps about 22 bits of it, 1 rounds once
 //   SUM          whether every tile's sums are added by themselves (mma_parts)
-//   ODD          whether values that are not finite stay with the rows that see their keys, and scales that no
-//                row sees are left out of vs.  Without it every finite scale of a tile counts.
+//   COPY         the tile's scales are lifted once, into 256 bytes of the warp's own at `copy`, where scales that no
+//                row sees are left out and values that are not finite stay with the rows that see them.  Without
+//                it they are lifted where they are used (which measured faster in the single-sequence kernel: a
+//                131,072-token layer 49.2 us against 50.3) and every finite scale of a tile counts.
 //   qfrag(b, f)  fills f[k-step] with the query's B fragments of block b (hi0, hi1, lo0, lo1)
 //   qsb_hi, lo   zero-point keys: the query's block sums as a B fragment (tile_scores)
 //   crow         turns a dot product with the normalised row into a base-2 softmax score
@@ -425,8 +448,8 @@ __device__ __forceinline__ void tile_scale_range(uint2 d, uint2 m, bool lo, bool
 //   m_run        the rows' references (above), vs the scales' state; l_run, oacc and racc are sums relative to
 //                them: of P, of P x scale x code (x vs.mul()) and of P x minimum
 // The tile is tile G of the copy at kb (K) and vb (V), arranged as L.
-template <typename L, int KF, int VF, int QP, int QSUM, bool SUM, bool ODD, typename QFrag, typename Mask>
-__device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int g, int t, QFrag qfrag,
+template <typename L, int KF, int VF, int QP, int QSUM, bool SUM, bool COPY, typename QFrag, typename Mask>
+__device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, uint32_t copy, int G, int g, int t, QFrag qfrag,
                                             uint32_t qsb_hi, uint32_t qsb_lo, const float (&crow)[2], Mask mask,
                                             ValueScale& vs, float (&m_run)[2], float (&l_run)[2],
                                             float (&oacc)[2 * kTileBlocks][4], float (&racc)[4]) {
@@ -440,11 +463,10 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
   // within 2^kGrow of what the running maximum asks for, so the exact cross-lane maximum is computed
   // only when some lane sees a score above it: one warp vote per tile (which the scales of the
   // tile's values share) instead of three shuffles per row.
-  const uint2 dv = lds_pair(vb + L::kVScale + ((G * 4 + t) * 8 + g) * 8);  // block g, tokens 2t, + 1, + 8, + 9
-  const uint2 mv = F::kVMin ? lds_pair(vb + L::kVMinimum + ((G * 4 + t) * 8 + g) * 8) : make_uint2(0u, 0u);
+  TileScales ts;
+  ts.load<L, F::kVMin>(vb, G, g, t);
   float sv[4], lm[2];
-  bool need = exceeds(dv.x, dv.y, vs.bound);
-  if constexpr (F::kVMin && ODD) need |= exceeds(mv.x, mv.y, 0x7BFF7BFFu);
+  bool need = ts.unusual<F::kVMin && COPY>(vs);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     sv[e] = mask(e, sacc[0][e] * crow[e & 1]);
@@ -454,16 +476,27 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
     lm[c] = fmaxf(sv[c], sv[c + 2]);
     need |= lm[c] > m_run[c] + vs.top;
   }
-  bool odd = false;  // a scale or minimum that is not finite, or a scale that no row sees above the bound
   if (__any_sync(0xffffffffu, need)) {
-    uint32_t seen, all;
-    tile_scale_range<ODD>(dv, mv, sv[0] != -INFINITY || sv[1] != -INFINITY, sv[2] != -INFINITY || sv[3] != -INFINITY, t,
-                          &seen, &all);
+    uint32_t most;
+    if constexpr (COPY) {
+      const uint32_t bad = ts.clean(sv[0] != -INFINITY || sv[1] != -INFINITY, sv[2] != -INFINITY || sv[3] != -INFINITY,
+                                    t, &most);
+      if (__any_sync(0xffffffffu, bad != 0)) {
+        uint32_t blind[2] = {0u, 0u};
+        blind_blocks(bad, sv, t, blind);
+#pragma unroll
+        for (int mt = 0; mt < 2 * kTileBlocks; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (blind[e & 1] >> (4 * (mt >> 1)) & 1u) oacc[mt][e] = NAN;
+      }
+    } else {
+      most = ts.largest();
+    }
     const float top = vs.top;
     int dk;
     float ratio;
-    vs.raise(seen, &dk, &ratio);
-    if constexpr (ODD) odd = all > (vs.bound & 0xFFFFu);
+    vs.raise(most, &dk, &ratio);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float mx = lm[c];
@@ -482,6 +515,11 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
       m_run[c] = m;
     }
   }
+  const uint32_t mul = vs.mul(), scales = COPY ? copy : vb + L::kVScale + G * 256;
+  if constexpr (COPY) {
+    ts.lift(vs, copy, g, t);
+    __syncwarp();
+  }
   // P as f16 parts, transposed in registers into B fragments
   uint32_t pbh[2], pbl[2];
   float pr[4];
@@ -491,10 +529,6 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
     pr[c] = fast_exp2(sv[c] - mu);
     pr[c + 2] = fast_exp2(sv[c + 2] - mu);
     l_run[c] += pr[c] + pr[c + 2];
-  }
-  if (odd) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) pr[e] = seen_p(pr[e], sv[e]);
   }
   {
     uint32_t h01, l01, h23, l23;
@@ -508,46 +542,21 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb, int G, int
   // ---------------- O^T += V^T P^T ----------------
   // V codes enter the MMA exactly; the per-token block scale multiplies P (in two f16 parts),
   // two MMAs per 16-dimension half.
-  const uint32_t mul = vs.mul();
-  auto add_values = [&](auto odd_tile) {
 #pragma unroll
-    for (int C = 0; C < kTileBlocks / 2; ++C)
-      tile_value_pair<L, KF, VF>(vb, G, C, g, t,
-                                 [&](int bl, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
-        uint32_t bh0, bl0, bh1, bl1;
-        scale_p<decltype(odd_tile)::value>(pbh[0], pbl[0], hmul2(d0, mul), bh0, bl0);
-        scale_p<decltype(odd_tile)::value>(pbh[1], pbl[1], hmul2(d1, mul), bh1, bl1);
-        mma_parts<SUM>(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1, bl0, bl1);
-        mma_parts<SUM>(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1, bl0, bl1);
-      });
-  };
-  if (odd)
-    add_values(std::true_type{});
-  else
-    add_values(std::false_type{});
+  for (int C = 0; C < kTileBlocks / 2; ++C)
+    tile_value_pair<L, KF, VF>(vb, scales, G, C, g, t,
+                               [&](int bl, const uint32_t (&a0)[4], const uint32_t (&a1)[4], uint32_t d0, uint32_t d1) {
+      uint32_t bh0, bl0, bh1, bl1;
+      split_scaled(pbh[0], pbl[0], COPY ? d0 : hmul2(d0, mul), bh0, bl0);
+      split_scaled(pbh[1], pbl[1], COPY ? d1 : hmul2(d1, mul), bh1, bl1);
+      mma_parts<SUM>(oacc[2 * bl], a0[0], a0[1], a0[2], a0[3], bh0, bh1, bl0, bl1);
+      mma_parts<SUM>(oacc[2 * bl + 1], a1[0], a1[1], a1[2], a1[3], bh0, bh1, bl0, bl1);
+    });
   if constexpr (F::kVMin) {
     // sum over the tile's tokens of p * m for all 8 blocks at once: A = the minima
     // (block g x tokens 2t, 2t + 1 | 2t + 8, 2t + 9, exact in f16; blocks 8..15 zero),
     // B = P^T as its high and low parts
-    uint32_t m01 = mv.x, m89 = mv.y;
-    if (odd) {
-      // a row of A meets every query row: minima that are not finite are added by hand, to the rows that see
-      // them (block g, rows 2t, 2t + 1)
-      m01 &= finite_halves(m01);
-      m89 &= finite_halves(m89);
-#pragma unroll 1
-      for (int tok = 0; tok < 16; ++tok) {
-        const int from = (tok & 7) * 4 + t;
-        const float p0 = __shfl_sync(0xffffffffu, tok < 8 ? pr[0] : pr[2], from);
-        const float p1 = __shfl_sync(0xffffffffu, tok < 8 ? pr[1] : pr[3], from);
-        const uint32_t word = lds32(vb + L::kVMinimum + (((G * 4 + (tok & 7) / 2) * 8 + g) * 4 + 2 * (tok >> 3)) * 2);
-        const float x = tok & 1 ? half_hi(word) : half_lo(word);
-        if (fabsf(x) <= 65504.f) continue;
-        if (p0 != 0.f) racc[0] += x;
-        if (p1 != 0.f) racc[1] += x;
-      }
-    }
-    mma_parts<SUM>(racc, m01, 0u, m89, 0u, pbh[0], pbh[1], pbl[0], pbl[1]);
+    mma_parts<SUM>(racc, ts.m.x, 0u, ts.m.y, 0u, pbh[0], pbh[1], pbl[0], pbl[1]);
   }
 }
 
