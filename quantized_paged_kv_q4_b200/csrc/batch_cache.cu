@@ -9,11 +9,12 @@
 // tokens), which takes four shuffles per block and eight tokens.
 //
 // Reading is bound by HBM: 131,072 tokens of 4 KV heads (Q8_0 / Q4_0, 218 MB) into bf16 (537 MB)
-// take 124 us, 0.94 of the measured copy bandwidth.  Writing a whole tile costs about 1,250
+// take 123 us, 0.95 of the measured copy bandwidth.  Writing a whole tile costs about 1,250
 // instructions a quarter (scales by IEEE division and reciprocal, codes by the format's own fp32
-// steps): six prompts of 100 to 4,000 tokens (28 MB of bf16 rows, 8 MB of pages) take 19 us, a
-// third of the copy bandwidth, bound by instruction issue (0.64 per cycle) and by one and a half
-// waves of CTAs.  One to eight tokens take 3 us a call, latency alone.
+// steps): six prompts of 100 to 4,000 tokens (28 MB of bf16 rows, 8 MB of pages) take 20 us, a
+// third of the copy bandwidth.  A warp encodes K and then V, both loaded from the start, so that 39 % of
+// the warps are active (64 registers; 91 for fp32 rows) and issue 0.64 instructions a cycle, in one and a
+// half waves of CTAs.  One to eight tokens take 3 us a call, latency alone.
 // Measured on the way: one warp per (row, head), with its byte stores and strided page reads: 215 us
 // for the 131,072 tokens; a whole tile a warp: 49.8 us to write the six prompts and read them back
 // (25.7 us in quarters).  Not kept: codes made by adding 2^23 with downward rounding and packed by

@@ -24,13 +24,18 @@
 // a fixed order.  A group has at most two partials, its first unit's and its last's, so the
 // workspace has two slots per group.
 //
-// What bounds it.  With 8 rows and bf16 a tile takes a warp about 565 instructions, and twelve warps
-// a SM keep up with HBM: eight sequences of 131,072 tokens (1.745 GB, Q8_0 / Q4_0) take 270 to 285
-// us in short runs, 0.95 to 1.0 of the measured copy bandwidth, and 320 us in a run of half a second,
-// where the 1,000 W cap brings the SM clock to 1.57 GHz.  With 24 rows a tile takes 1,200
-// instructions at 0.46 a cycle (dependent instructions, shared-memory latency, the pace of mma.sync):
-// eight verify steps of four tokens (149 MB) take 63 us, 0.36.  Short batches are bound by latency: the
-// plan 2.4 us, pages and queries 3 us, then 1.5 to 2 us a tile and group, and the merge grid.
+// What bounds it.  With 8 rows and bf16 a tile takes a warp about 690 instructions: eight sequences of
+// 131,072 tokens (1.745 GB, Q8_0 / Q4_0) take 288 to 293 us in short runs, 0.92 to 0.94 of the measured copy
+// bandwidth, and 331 us back to back, 0.82, where the 1,000 W cap lowers the SM clock.  fp32 (the query's second
+// part, sums added tile by tile) is bound by its arithmetic: 433 us.  With 24 rows a tile takes 1,500
+// instructions at 0.46 a cycle (dependent instructions, the pace of mma.sync, shared-memory latency, two
+// barriers a step): eight verify steps of four tokens (149 MB) take 78 us, 0.30 of that bandwidth.  Short batches are bound
+// by latency: the plan 2.4 us, pages and queries 3 us, then 1.5 to 2 us a tile and group, and the merge grid.
+//
+// What precision costs (one run, captured graphs; the three figures are 8 x 131,072, 32 ragged and 8
+// verify steps in bf16).  P in one f16 part, P x scale as it comes: 264, 39.8, 64.2 us, with errors of 3e-4
+// before the store, and of percents where a dominant key meets small values.  P in two parts: 286,
+// 42.9, 75.4.  With the powers of two, and what is not finite told apart: 288, 41.2, 77.8.
 //
 // Not kept: a CTA of four groups on one stretch, their states merged through shared memory at the
 // end of each unit (2 to 4 us of barriers a unit: 32 ragged sequences of up to 16,384 tokens in
@@ -118,8 +123,8 @@ struct BatchCfg {
   static constexpr int kSmemBytes = kMetaOff + kBatchMeta;
   static_assert(kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
   static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
-  // What a unit costs beside its tiles, and the least a group takes, in tiles.  Units: 32 ragged
-  // sequences in 41.3 us with 2, 38.8 with 4.  Shares: 1 x 4,096 tokens in 17.1 us with 4, 15.0 with 2
+  // What a unit costs beside its tiles, and the least a group takes, in tiles (both measured with P in one
+  // f16 part).  Units: 32 ragged sequences in 41.3 us with 2, 38.8 with 4.  Shares: 1 x 4,096 tokens in 17.1 us with 4, 15.0 with 2
   // (128 groups of two tiles and a merge of 128 parts).
   static constexpr int kUnitCost = 4, kMinShare = 2;
 };
@@ -158,9 +163,9 @@ struct WideCfg {
   static constexpr int kSmemBytes = kMetaOff + kBatchMeta;
   static_assert(kGroups >= 1 && kStages >= 2 && kMetaOff <= kBatchRoom && kGroupBytes % 16 == 0, "shared memory");
   static_assert(kWarps * kStages * 4 + sizeof(BatchPlanState<kWarps, kGroups>) <= kBatchMeta, "meta");
-  // 48 windowed sequences in 38.2, 35.6 and 37.8 us with (3, 4), (6, 8) and (10, 16), eight verify
-  // steps in 65.5, 63.5 and 62.2.  With 7 a unit of one tile fills a share: 16 sequences of one to
-  // four tokens in 14.5 us, with 8 (two units in some groups) in 21.2
+  // With P in one f16 part: 48 windowed sequences in 38.2, 35.6 and 37.8 us with (3, 4), (6, 8) and (10,
+  // 16), eight verify steps in 65.5, 63.5 and 62.2.  With 7 a unit of one tile fills a share: 16 sequences of
+  // one to four tokens in 14.5 us, with 8 (two units in some groups) in 21.2
   static constexpr int kUnitCost = 6, kMinShare = 7;
 };
 

@@ -316,20 +316,23 @@ __device__ __forceinline__ void tile_value_pair(uint32_t vb, uint32_t scales, in
 //           they stay as they are, and k is its exponent instead (a small scale then keeps its bits)
 // The products' two parts so end about 2^37 below the row's largest P times the largest scale.
 // (Both are one state of all rows and channels that a warp, or a group of warps, adds up.  It moves when a
-// larger scale of a key that some row sees comes along: seldom after the first tiles.)
+// larger scale comes along: seldom after the first tiles.  Single-sequence decode of 131,072 tokens: 47.7 us
+// a layer without all this, 48.6 with it.)
 constexpr float kPTop = 13.f, kGrow = 2.f;
 
 struct ValueScale {
-  uint32_t bound = 0u;          // twice the f16 power of two that no scale so far exceeds (0: none seen)
+  uint32_t bound = 0u;          // in both halves, the f16 power of two that no scale so far exceeds (0: none seen)
   float top = kPTop + kGrow;    // how far a score may pass its row's reference: kPTop + kGrow - k
   __device__ __forceinline__ uint32_t mul() const { return 0x78007800u - min(bound, 0x3C003C00u); }
   // the exponent of the bound, + 15 (2^16 is kept as the largest f16 instead, so that infinities exceed it)
   __device__ __forceinline__ int exponent() const { return static_cast<int>((bound & 0xFFFFu) + 0x3FFu) >> 10; }
   // what undoes mul() in a sum
   __device__ __forceinline__ float unit() const { return exp2_int(min(exponent(), 15) - 15); }
-  __device__ __forceinline__ static float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-  // Takes in scales up to `most` (f16 bits): the new exponent of two of the rows' references goes to *k, the
-  // factor of the sums of P x scale beside it to *ratio.
+  __device__ __forceinline__ static float exp2_int(int e) {
+    return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  }
+  // Takes in scales up to `most` (f16 bits): what the rows' references rise by goes to *dk, the factor of the
+  // sums of P x scale beside that to *ratio.
   __device__ __forceinline__ void raise(uint32_t most, int* dk, float* ratio) {
     const int was = exponent();
     int now = was;
