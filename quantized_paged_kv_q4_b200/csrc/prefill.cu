@@ -719,6 +719,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1) prefill_kernel(const PrefillP
           }
         }
       }
+      // The stage goes back to the copy engine: every lane's reads (generic proxy) come before the refill
+      // (async proxy).  Their values are not used yet, so that nothing else makes the warp wait for them.
+      tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&rawempty[r]);
       // ---------------- K^ (this CTA's buffer is free once QK(j - 3) completed) ----
